@@ -1,0 +1,407 @@
+// The 8-bit format beside the 4-bit layer ("FP8 block-128"): E4M3 codes with
+// one power-of-two scale (E8M0, byte b = 2^(b - 127)) per 128 consecutive
+// elements along K, and the pieces its kernels share.
+//
+// A block of values v with amax = max |v_i| takes the smallest scale 2^e,
+// e >= -127, with amax <= 448 2^e, and the codes E4M3_RNE(v_i 2^-e).  A power
+// of two costs no precision (the scaling is exact, and E4M3's own exponent
+// absorbs up to one bit of headroom), never saturates, and is what the tensor
+// cores multiply in by themselves: with an fp32 scale per block every 128 of K
+// would have to leave tensor memory to be scaled on the CUDA cores.
+#pragma once
+
+#include "common.cuh"
+
+namespace svdq {
+
+constexpr int kFp8Block = 128;
+
+// Blocks per row, and the 512-byte scale tiles (128 rows x 4 blocks) per
+// 128-row band.
+__host__ __device__ __forceinline__ int64_t fp8_blocks(int64_t K) { return (K + 127) >> 7; }
+__host__ __device__ __forceinline__ int64_t fp8_band_tiles(int64_t K) { return (K + 511) >> 9; }
+
+// Byte offset of the scale of (row, block) in the tile layout; the four
+// blocks 4 j .. 4 j + 3 of a row are consecutive.
+__device__ __forceinline__ size_t fp8_scale_offset(int64_t row, int blk, int64_t band_tiles) {
+  return (static_cast<size_t>(row >> 7) * static_cast<size_t>(band_tiles) + (blk >> 2)) * 512 +
+         (static_cast<size_t>(row) & 31) * 16 + ((static_cast<size_t>(row) & 127) >> 5) * 4 + (blk & 3);
+}
+
+// The scale byte of a block.  amax = 2^(E - 127) (1 + f) needs
+// e = E - 127 - 8 (448 = 1.75 2^8), one more when f > 0.75: adding 2^21 - 1 to
+// the bits carries into the exponent exactly then.  Zero and tiny blocks clamp
+// at b = 0; infinity gives b = 247.
+__device__ __forceinline__ uint32_t fp8_scale_byte(float amax) {
+  const int b = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
+  return static_cast<uint32_t>(max(b, 0));
+}
+
+// 2^-e for a scale byte in [0, 247]: always a normal fp32 number.
+__device__ __forceinline__ float fp8_inv_scale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// Four fp32 values -> four E4M3 codes, element i in byte i (round to nearest
+// even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
+}
+
+// Packed fp32 pairs (one instruction for both halves).
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---------------------------------------------------------------- GELU ----
+// GELU(x) = x Phi(x) = max(x, 0) - |x| Phi(-|x|), which has no cancellation
+// for negative x, so the result is good to about 1e-6 relative everywhere
+// (an error against the block's largest value would be too little: small
+// values keep their own E4M3 exponent).
+//
+// |x| <= 5.5:  Phi(-z) = 2^g(z), g = log2 Phi(-z) as a polynomial of degree
+// 10: one exponential an element and no division (measured on B200: see
+// quantize_fp8_kernel).  The coefficients are this project's own fit: minimax
+// in g (reweighted least squares on Chebyshev nodes, |error| 1.3e-7 in
+// ln Phi), rounded to fp32.
+// |x| > 5.5 (rare; a warp-uniform branch): Phi(-z) = 2^(-z^2 log2(e) / 2) t P(t),
+// t = 1 / (1 + 0.3 z), P of degree 7 fitted to 0.5 erfcx(z / sqrt 2) / t with
+// relative error 1.3e-7 up to z = 13.5, where 2^(...) leaves the fp32 range.
+// The last step rounds toward zero: beyond 5.5 the exact result is below x by
+// less than half an ulp, and rounding up to x itself would turn an E4M3 tie
+// the wrong way.
+constexpr float kGeluFast = 5.5f;
+
+__device__ __forceinline__ float gelu_tail(float x) {
+  const float z = fabsf(x);
+  const float zc = fminf(z, 13.5f);
+  const float t = rcp_approx(__fmaf_rn(zc, 0.3f, 1.0f));
+  float q = 0.03593172878026962f;
+  q = __fmaf_rn(q, t, -0.15827596187591553f);
+  q = __fmaf_rn(q, t, 0.20820654928684235f);
+  q = __fmaf_rn(q, t, -0.055393803864717484f);
+  q = __fmaf_rn(q, t, 0.12946918606758118f);
+  q = __fmaf_rn(q, t, 0.09963750094175339f);
+  q = __fmaf_rn(q, t, 0.12079835683107376f);
+  q = __fmaf_rn(q, t, 0.11962638795375824f);
+  q = __fmul_rn(__fmul_rn(q, t), ex2_approx(__fmul_rn(__fmul_rn(zc, zc), -0.72134752044448170f)));
+  return __fmaf_rz(-z, q, fmaxf(x, 0.0f));
+}
+
+__device__ __forceinline__ void gelu2_fast(float& x0, float& x1) {
+  const float z0 = fabsf(x0), z1 = fabsf(x1);
+  const uint64_t z = pack_f32x2(fminf(z0, kGeluFast), fminf(z1, kGeluFast));
+  constexpr float c[11] = {-0.9999998211860657f,     -1.1511125564575195f,    -0.4591609537601471f,
+                           -0.05260409042239189f,    0.007166661322116852f,   -0.00016647009761072695f,
+                           -0.0002045672881649807f,  5.589646752923727e-05f,  -7.6225755947234575e-06f,
+                           5.619402827505837e-07f,   -1.7772931570902983e-08f};
+  uint64_t g = pack_f32x2(c[10], c[10]);
+#pragma unroll
+  for (int i = 9; i >= 0; --i) g = fma_f32x2(g, z, pack_f32x2(c[i], c[i]));
+  float g0, g1;
+  unpack_f32x2(g, g0, g1);
+  x0 = __fmaf_rz(-z0, ex2_approx(g0), fmaxf(x0, 0.0f));
+  x1 = __fmaf_rz(-z1, ex2_approx(g1), fmaxf(x1, 0.0f));
+}
+
+// GELU of n values in registers (n even); all lanes of the warp call it.
+template <int n>
+__device__ __forceinline__ void gelu_n(float* v) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < n; ++i) top = fmaxf(top, fabsf(v[i]));
+  if (__any_sync(0xffffffffu, top > kGeluFast)) {
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+      float a = v[i], b = v[i + 1];
+      gelu2_fast(a, b);
+      v[i] = fabsf(v[i]) > kGeluFast ? gelu_tail(v[i]) : a;
+      v[i + 1] = fabsf(v[i + 1]) > kGeluFast ? gelu_tail(v[i + 1]) : b;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; i += 2) gelu2_fast(v[i], v[i + 1]);
+  }
+}
+
+// ------------------------------------------------------------- elements ----
+// Eight consecutive elements of a row.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo(w.x);
+  v[1] = bf16_hi(w.x);
+  v[2] = bf16_lo(w.y);
+  v[3] = bf16_hi(w.y);
+  v[4] = bf16_lo(w.z);
+  v[5] = bf16_hi(w.z);
+  v[6] = bf16_lo(w.w);
+  v[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+  v[4] = b.x;
+  v[5] = b.y;
+  v[6] = b.z;
+  v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                            pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float amax8(const float* v) {
+  return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+               fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+}
+__device__ __forceinline__ uint2 codes8(const float* v, float inv) {
+  return make_uint2(cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+// Maximum over the 16 lanes that hold one block (8 elements each).
+__device__ __forceinline__ float block_max16(float a) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+
+// Zero scales of the padding rows [M, ceil(M / 128) 128): a word of four
+// blocks at a time, by `threads` threads.
+__device__ __forceinline__ void zero_pad_scales(uint8_t* scales, int64_t M, int64_t band_tiles, int tid, int threads) {
+  const int64_t pad = ((M + 127) & ~int64_t(127)) - M;
+  for (int64_t i = tid; i < pad * band_tiles; i += threads)
+    *reinterpret_cast<uint32_t*>(scales + fp8_scale_offset(M + i / band_tiles, static_cast<int>(i % band_tiles) * 4,
+                                                           band_tiles)) = 0;
+}
+
+// ============================================================ quantiser ====
+// x codes and scales of X (or GELU(X)), bf16 [M][K] with row stride ldx.
+// Thread = 8 columns of kQ8Rows consecutive rows (one 16-byte load each, all
+// in flight together), 16 lanes = one block.  HBM-bound: 2 + 1 bytes an
+// element.  The grid's last x index zeroes the padding rows' scales.
+constexpr int kQ8Threads = 256;
+constexpr int kQ8Rows = 4;
+
+template <bool GELU>
+__global__ void __launch_bounds__(kQ8Threads)
+    quantize_fp8_kernel(const __nv_bfloat16* __restrict__ X, int64_t ldx, int M, int K, uint8_t* __restrict__ codes,
+                        uint8_t* __restrict__ scales) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t band_tiles = fp8_band_tiles(K);
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y == 0) zero_pad_scales(scales, M, band_tiles, threadIdx.x, kQ8Threads);
+    return;
+  }
+  const int c8 = blockIdx.y * kQ8Threads + threadIdx.x;  // 8-column chunk
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kQ8Rows;
+  const int blk = c8 >> 4;
+  if (blk >= 4 * band_tiles) return;                     // whole 16-lane groups, and whole warps unless K ends in one
+  const bool in = 8 * c8 < K;
+  float v[kQ8Rows][8];
+#pragma unroll
+  for (int i = 0; i < kQ8Rows; ++i) {
+    if (in && row0 + i < M) {
+      load8(X + (row0 + i) * ldx + 8 * c8, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kQ8Rows; ++i) {
+    if (row0 + i >= M) break;
+    if constexpr (GELU) gelu_n<8>(v[i]);
+    const uint32_t b = fp8_scale_byte(block_max16(amax8(v[i])));
+    if (in) *reinterpret_cast<uint2*>(codes + (row0 + i) * K + 8 * c8) = codes8(v[i], fp8_inv_scale(b));
+    if ((c8 & 15) == 0) scales[fp8_scale_offset(row0 + i, blk, band_tiles)] = static_cast<uint8_t>(b);
+  }
+}
+
+// ============================================================ RMS norm ====
+// h = X + residual (stored back), y = h rsqrt(mean(h^2) + eps) gamma, written
+// as FP8 block-128 and / or as bf16, from one read of X and the residual.
+// The norm is taken of the stored h (rounded to the residual's type), so the
+// result is the same whether or not the addition is fused.  The row's sum of
+// squares, the root and the product stay in fp32 until the one rounding of
+// each output.
+//
+// One CTA per row; thread = V chunks of 8 columns kept in registers between
+// the reduction and the outputs, 16 lanes = one block.  The CTA behind the last row zeroes
+// the padding rows' scales.
+template <int V, typename RES>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_kernel(const __nv_bfloat16* X, int64_t ldx, const RES* residual, const __nv_bfloat16* __restrict__ gamma,
+                   float eps, int M, int K, RES* residual_out, __nv_bfloat16* Y, uint8_t* __restrict__ codes,
+                   uint8_t* __restrict__ scales) {
+  __shared__ float part[32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, T = blockDim.x;
+  const int64_t band_tiles = fp8_band_tiles(K);
+  const int64_t row = blockIdx.x;
+  if (row == M) {
+    if (scales) zero_pad_scales(scales, M, band_tiles, tid, T);
+    return;
+  }
+  const int chunks = K >> 3;
+  float h[V][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * T;
+    if (c < chunks) {
+      load8(X + row * ldx + 8 * c, h[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+    }
+  }
+  if (residual) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * T;
+      if (c < chunks) {
+        float r[8];
+        load8(residual + row * K + 8 * c, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[i][e] = __fadd_rn(h[i][e], r[e]);
+          if constexpr (sizeof(RES) == 2) h[i][e] = __bfloat162float(__float2bfloat16_rn(h[i][e]));
+        }
+        store8(residual_out + row * K + 8 * c, h[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __fmaf_rn(h[i][e], h[i][e], ss);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if ((tid & 31) == 0) part[tid >> 5] = ss;
+  __syncthreads();
+  float sum = (tid & 31) < (T >> 5) ? part[tid & 31] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(K)), eps));
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = tid + i * T;
+    const bool in = c < chunks;
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(h[i][e], rstd);
+    if (gamma && in) {
+      float g[8];
+      load8(gamma + 8 * c, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(y[e], g[e]);
+    }
+    if (Y && in) store8(Y + row * K + 8 * c, y);
+    if (codes) {
+      const uint32_t b = fp8_scale_byte(block_max16(amax8(y)));
+      if (in) *reinterpret_cast<uint2*>(codes + row * K + 8 * c) = codes8(y, fp8_inv_scale(b));
+      const int blk = c >> 4;
+      if ((c & 15) == 0 && blk < 4 * band_tiles) scales[fp8_scale_offset(row, blk, band_tiles)] = static_cast<uint8_t>(b);
+    }
+  }
+  if (codes) {
+    // scale bytes of the row's last word that no thread's chunk reaches
+    const int reach = (T * V + 15) >> 4;
+    for (int blk = reach + tid; blk < 4 * band_tiles; blk += T) scales[fp8_scale_offset(row, blk, band_tiles)] = 0;
+  }
+}
+
+// ======================================================== weight packer ====
+// W [K][N] (row-major, as the layer's residual) -> codes [N][K] and scales:
+// one row per output channel, blocks along K.  A CTA transposes 128 (K) x 64
+// (N) through shared memory; 4 threads quantise one output row's block (32
+// values each) and write its 128 code bytes.  HBM-bound: sizeof(T) + 1 bytes an
+// element, once per weight.
+constexpr int kPw8Threads = 256;
+constexpr int kPw8N = 64;
+
+template <typename T>
+__global__ void __launch_bounds__(kPw8Threads)
+    pack_weight_fp8_kernel(const T* __restrict__ W, int K, int N, uint8_t* __restrict__ codes,
+                           uint8_t* __restrict__ scales) {
+  __shared__ float tile[kFp8Block][kPw8N + 1];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x;
+  const int n0 = blockIdx.x * kPw8N;
+  const int blk = blockIdx.y;  // up to the last block of the last scale tile: those past K are zero scales
+  const int k0 = blk * kFp8Block;
+  const int64_t band_tiles = fp8_band_tiles(K);
+  for (int i = tid; i < kFp8Block * (kPw8N / 8); i += kPw8Threads) {
+    const int k = i / (kPw8N / 8), n = 8 * (i % (kPw8N / 8));
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (k0 + k < K && n0 + n < N) load8(W + static_cast<int64_t>(k0 + k) * N + n0 + n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[k][n + e] = v[e];
+  }
+  __syncthreads();
+  const int n = tid >> 2, part = tid & 3;  // 32 values: k = 32 part ...
+  float v[32];
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = tile[32 * part + i][n];
+    a = fmaxf(a, fabsf(v[i]));
+  }
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  const uint32_t b = fp8_scale_byte(a);
+  const float inv = fp8_inv_scale(b);
+  const int64_t row = n0 + n;
+  if (row < N) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // K is a multiple of 16: a 16-byte store is inside or outside
+      const int k = k0 + 32 * part + 16 * j;
+      const float* s = v + 16 * j;
+      if (k < K)
+        *reinterpret_cast<uint4*>(codes + row * K + k) = make_uint4(
+            cvt_e4m3x4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv),
+            cvt_e4m3x4(s[4] * inv, s[5] * inv, s[6] * inv, s[7] * inv),
+            cvt_e4m3x4(s[8] * inv, s[9] * inv, s[10] * inv, s[11] * inv),
+            cvt_e4m3x4(s[12] * inv, s[13] * inv, s[14] * inv, s[15] * inv));
+    }
+  }
+  // rows past N are zeros in the tile: their scale byte is 0
+  if (part == 0 && row < ((static_cast<int64_t>(N) + 127) & ~int64_t(127)))
+    scales[fp8_scale_offset(row, blk, band_tiles)] = static_cast<uint8_t>(b);
+}
+
+}  // namespace svdq

@@ -1,0 +1,358 @@
+// 8-bit linear in the FP8 block-128 format for sm_100a, large-M path:
+// Y = deq(x) deq(w)^T + bias as bf16, or GELU of it quantised to the next
+// layer's FP8 input.  The tensor cores apply both power-of-two scales
+// themselves (kind::mxf8f6f4, one UE8M0 scale per 32 along K: the byte of a
+// 128-block serves its four 32-blocks), so a tile accumulates over all of K in
+// tensor memory.
+#pragma once
+
+#include "fp8.cuh"
+
+namespace svdq {
+
+// Persistent CTA pairs (clusters of 2): grid = 2 x min(pair tiles, SMs / 2),
+// 192 threads per CTA: warp 0 TMA producer, warp 1 TMEM owner and (even CTA)
+// MMA issuer, warps 2-5 epilogue; the roles, the hand-offs and the abort
+// drain are those of the 4-bit kernel (linear.cuh).
+// A pair computes 256 x 256 output tiles, visited M-fastest; CTA c holds 128
+// of the tile's x rows and 128 of its w rows, the even CTA issues 2-SM MMAs
+// (M = 256, N = 256, K = 32).
+// Ring: 6 stages of 128 columns of K per CTA (x codes and w codes, 128 rows x
+// 128 bytes each, 128-byte swizzle).  Every fourth stage of a tile also brings
+// the scale tiles of its 512 columns (this CTA's x rows; all 256 w rows), and
+// the MMA warp copies them into one of two scale regions of tensor memory
+// with three tcgen05.cp per 512 columns; stage j of the four selects byte j of
+// each scale word through the instruction descriptor.  (At one scale per 16
+// the 4-bit kernel needs twelve copies per 256 columns, the largest single
+// cost of its tensor pipe.)  The tensor pipe runs a thread's copies and MMAs
+// in order, so the regions alternate without a barrier.
+// Accumulators: two 128 x 256 fp32 tiles overlap in each CTA's TMEM as in the
+// 4-bit kernel: columns [0, 256) and [192, 448), scales in [448, 480).
+constexpr int kL8Threads = 192;
+constexpr int kL8Stages = 6;
+constexpr int kL8BM = 256, kL8BN = 256, kL8BK = 128;
+constexpr uint32_t kL8ABytes = 16384, kL8BBytes = 16384;
+constexpr uint32_t kL8StageBytes = kL8ABytes + kL8BBytes;
+constexpr uint32_t kL8SfBytes = 512 + 1024;           // a stage's scale tiles
+constexpr uint32_t kL8SfOffset = kL8Stages * kL8StageBytes;
+constexpr uint32_t kL8BiasOffset = kL8SfOffset + kL8Stages * kL8SfBytes;
+constexpr uint32_t kL8OutOffset = kL8BiasOffset + 1024;
+constexpr uint32_t kL8OutBytes = 4096;                // one warp's 32 rows x 128 bytes of output
+constexpr uint32_t kL8BarOffset = kL8OutOffset + 4 * kL8OutBytes;
+constexpr int kL8NumBars = 2 * kL8Stages + 2 + 2 + 1 + 1 + 1;
+constexpr uint32_t kL8TmemCols = 512;
+constexpr uint32_t kL8Acc1Col = 192;
+constexpr uint32_t kL8SfCol = 448;                    // region p: x scales at +16 p, w scales at +16 p + 8
+
+struct L8Params {
+  const __nv_bfloat16* bias;
+  uint8_t* y_scales;   // FP8 output: scale tiles of the output rows
+  int M, K, N;
+  int m_tiles, tiles;  // pair tiles: ceil(M / 256) x ceil(N / 256)
+  uint64_t timeout_ns;
+};
+
+// FP8_OUT: GELU and FP8 block-128 output (two blocks per tile row, each wholly
+// in one epilogue thread); otherwise bf16.
+template <bool FP8_OUT>
+__global__ void __launch_bounds__(kL8Threads, 1)
+    linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
+                      const __grid_constant__ CUtensorMap tm_y, const L8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  float* bias_s = reinterpret_cast<float*>(smem + kL8BiasOffset);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kL8BarOffset);
+  uint64_t* full = bars;                          // [S] even CTA: both CTAs' stage landed
+  uint64_t* empty = full + kL8Stages;             // [S] the stage's MMAs and copies are done
+  uint64_t* acc_full = empty + kL8Stages;         // [2] tile accumulated (both CTAs)
+  uint64_t* acc_empty = acc_full + 2;             // [2] even CTA: 8 epilogue warps drained it
+  uint64_t* ovl_free = acc_empty + 2;             // even CTA: shared columns drained
+  uint64_t* fin = ovl_free + 1;                   // even CTA: every MMA complete
+  uint64_t* odd_done = fin + 1;                   // even CTA: the odd producer published its count
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kL8NumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* odd_issued = tmem_slot + 2;  // even CTA: stages the odd producer issued
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();  // 0 = even CTA (MMA issuer)
+  const int pair = blockIdx.x >> 1;
+  const int pairs = gridDim.x >> 1;
+  const int N = p.N;
+  const int total = (p.K + kL8BK - 1) / kL8BK;    // stages per tile
+  const int band_tiles = (p.K + 511) >> 9;        // scale tiles per 128-row band
+
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kL8TmemCols);
+    tmem_relinquish_pair();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kL8Stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 8);
+    }
+    mbar_init(smem_u32(ovl_free), 8);
+    mbar_init(smem_u32(fin), 1);
+    mbar_init(smem_u32(odd_done), 1);
+    *odd_issued = 0;
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the even CTA's barriers exist before anyone signals them
+  tc_fence_after();
+  griddep_launch_dependents();  // with the tensor memory held (see ptx.cuh)
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  auto lead = [&](const uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
+  // bytes one CTA loads for stage `it` of a tile
+  auto stage_tx = [](int it) { return kL8StageBytes + ((it & 3) == 0 ? kL8SfBytes : 0u); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------- producer --
+    if (lane == 0) {
+      prefetch_tmap(&tm_x);
+      prefetch_tmap(&tm_w);
+      prefetch_tmap(&tm_xs);
+      prefetch_tmap(&tm_ws);
+    }
+    __syncwarp();
+    // While the kernel ahead finishes: the w codes of the ring's first stages into L2.
+    if (pair < p.tiles) {
+      const int nb = (pair / p.m_tiles) * kL8BN + 128 * static_cast<int>(rank);
+      for (int it = 0; it < min(total, kL8Stages); ++it) e_tma_prefetch_2d(&tm_w, it * kL8BK, nb);
+    }
+    griddep_wait();
+    uint32_t g = 0;
+    bool ok = true;
+    for (int t = pair; t < p.tiles && ok && !warp_flag(abort_flag); t += pairs) {
+      const int band = (t % p.m_tiles) * 2 + static_cast<int>(rank);  // this CTA's 128 rows
+      const int n0 = (t / p.m_tiles) * kL8BN;
+      for (int it = 0; it < total; ++it, ++g) {
+        const int s = g % kL8Stages;
+        ok = warp_wait(smem_u32(&empty[s]), ((g / kL8Stages) & 1) ^ 1, p.timeout_ns, 60);
+        if (!ok) {
+          *abort_flag = 1;
+          break;
+        }
+        const uint32_t fb = lead(&full[s]);
+        const uint32_t a_s = sbase + s * kL8StageBytes;
+        if (rank == 0) e_arrive_expect_tx(smem_u32(&full[s]), 2 * stage_tx(it));
+        e_tma_load_2d_pair(a_s, &tm_x, fb, it * kL8BK, band * 128);
+        e_tma_load_2d_pair(a_s + kL8ABytes, &tm_w, fb, it * kL8BK, n0 + 128 * static_cast<int>(rank));
+        if ((it & 3) == 0) {
+          // bands past the end of a tensor read zeros; their rows are never stored
+          const uint32_t sf = sbase + kL8SfOffset + s * kL8SfBytes;
+          const int st = it >> 2;
+          e_tma_load_3d_pair(sf, &tm_xs, fb, 0, 0, band * band_tiles + st);
+          e_tma_load_3d_pair(sf + 512, &tm_ws, fb, 0, 0, (n0 >> 7) * band_tiles + st);
+          e_tma_load_3d_pair(sf + 1024, &tm_ws, fb, 0, 0, ((n0 >> 7) + 1) * band_tiles + st);
+        }
+      }
+    }
+    // After an abort: both producers' copies complete on the even CTA's full[]
+    // barriers, which only the even producer arms; it makes every phase either
+    // CTA may still have in flight completable and waits for it (linear.cuh).
+    if (rank == 1) {
+      if (lane == 0) {
+        st_dsmem_u32(map_shared_rank(smem_u32(const_cast<uint32_t*>(odd_issued)), 0), g);
+        mbar_arrive_cluster(lead(odd_done));
+      }
+      __syncwarp();
+    } else if (warp_flag(abort_flag)) {
+      const bool have = warp_wait_cluster(smem_u32(odd_done), 0, 2 * p.timeout_ns + 100000000ull, 67);
+      const uint32_t g_odd = have ? __shfl_sync(0xffffffffu, *odd_issued, 0) : g;
+      const uint32_t hi = g > g_odd ? g : g_odd;
+      for (uint32_t j = hi > kL8Stages ? hi - kL8Stages : 0; j < hi; ++j) {
+        const uint32_t s = j % kL8Stages;
+        const uint32_t per_cta = stage_tx(static_cast<int>(j % static_cast<uint32_t>(total)));
+        if (j >= g) e_arrive_expect_tx(smem_u32(&full[s]), per_cta);           // only the odd CTA issued it
+        else if (j >= g_odd) e_mbar_complete_tx(smem_u32(&full[s]), per_cta);  // only this CTA issued it
+        warp_wait(smem_u32(&full[s]), (j / kL8Stages) & 1, p.timeout_ns, 66);
+      }
+    }
+  } else if (warp == 1) {
+    griddep_wait();  // bounded waits start once the kernel ahead is done
+    if (rank == 0) {
+      // -------------------------------------------------- MMA issuer --
+      // E4M3 x E4M3, UE8M0 scales; bits 4-5 and 29-30 select the scale bytes
+      const uint32_t idesc = (1u << 23) | ((kL8BN >> 3) << 17) | ((kL8BM >> 4) << 24);
+      uint32_t g = 0, sg = 0;  // stages; scale groups copied
+      int i = 0;
+      bool ok = true;
+      for (int t = pair; t < p.tiles && ok && !warp_flag(abort_flag); t += pairs, ++i) {
+        const int b = i & 1;
+        const uint32_t acc = tmem + (b ? kL8Acc1Col : 0u);
+        if (i >= 2) ok = warp_wait_cluster(smem_u32(&acc_empty[b]), ((i >> 1) - 1) & 1, p.timeout_ns, 61);
+        if (ok && i >= 1) ok = warp_wait_cluster(smem_u32(ovl_free), (i - 1) & 1, p.timeout_ns, 62);
+        if (!ok) break;
+        tc_fence_after();
+        for (int it = 0; it < total; ++it, ++g) {
+          const int s = g % kL8Stages;
+          ok = warp_wait(smem_u32(&full[s]), (g / kL8Stages) & 1, p.timeout_ns, 63);
+          if (!ok) break;
+          const uint32_t a_s = sbase + s * kL8StageBytes;
+          const uint32_t b_s = a_s + kL8ABytes;
+          tc_fence_after();
+          if ((it & 3) == 0) {
+            const uint32_t sf = sbase + kL8SfOffset + s * kL8SfBytes;
+            const uint32_t sft = tmem + kL8SfCol + 16 * (sg & 1);
+            e_tmem_cp_pair_32x128b_warpx4(sft, make_sdesc(sf, 0, 128, 0));
+            e_tmem_cp_pair_32x128b_warpx4(sft + 8, make_sdesc(sf + 512, 0, 128, 0));
+            e_tmem_cp_pair_32x128b_warpx4(sft + 12, make_sdesc(sf + 1024, 0, 128, 0));
+            ++sg;
+          }
+          const uint32_t sft = tmem + kL8SfCol + 16 * ((sg - 1) & 1);
+          const uint32_t id = idesc | (static_cast<uint32_t>(it & 3) << 4) | (static_cast<uint32_t>(it & 3) << 29);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            e_mma_mxf8_pair(acc, make_sdesc(a_s + kk * 32, 16, 1024, 2), make_sdesc(b_s + kk * 32, 16, 1024, 2), id,
+                            sft, sft + 8, (it > 0 || kk > 0) ? 1u : 0u);
+          e_commit_pair_both(smem_u32(&empty[s]));
+        }
+        e_commit_pair_both(smem_u32(&acc_full[b]));
+      }
+      if (!ok) *abort_flag = 1;
+      // own MMAs (which write both CTAs' tensor memory) complete before the
+      // pair may release it
+      e_commit_pair_both(smem_u32(fin));
+      if (!warp_wait(smem_u32(fin), 0, p.timeout_ns, 65)) *abort_flag = 1;
+    }
+  } else {
+    // ------------------------------------------------------- epilogue --
+    griddep_wait();            // the bias and Y may belong to the kernel ahead
+    const int et = tid - 64;   // 0..127
+    const int q = warp & 3;    // TMEM lane quadrant this warp may access
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    uint8_t* blk = smem + kL8OutOffset + (warp - 2) * kL8OutBytes;
+    uint8_t* rowp = blk + lane * 128;
+    int i = 0;
+    for (int t = pair; t < p.tiles; t += pairs, ++i) {
+      const int b = i & 1;
+      const int m0 = ((t % p.m_tiles) * 2 + static_cast<int>(rank)) * 128;
+      const int n0 = (t / p.m_tiles) * kL8BN;
+      named_bar_sync(1, 128);  // everyone is done with the previous tile's bias
+      for (int j = et; j < kL8BN; j += 128) {
+        const int n = n0 + j;
+        bias_s[j] = (p.bias && n < N) ? __bfloat162float(p.bias[n]) : 0.0f;
+      }
+      named_bar_sync(1, 128);
+      // no early exit: all four warps must keep meeting the named barriers
+      const bool ok = !warp_flag(abort_flag) && warp_wait(smem_u32(&acc_full[b]), (i >> 1) & 1, p.timeout_ns, 70);
+      if (!ok) {
+        *abort_flag = 1;
+        continue;
+      }
+      tc_fence_after();
+      const uint32_t acc_col = b ? kL8Acc1Col : 0u;
+      if constexpr (FP8_OUT) {
+        uint32_t sbytes = 0;
+#pragma unroll 1
+        for (int gi = 0; gi < 2; ++gi) {
+          // the 128-column block that holds the 64 shared columns first
+          const int h = b ? gi : 1 - gi;
+          float v[128];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 128 * h + 32 * j, reinterpret_cast<uint32_t*>(v) + 32 * j);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead(gi == 0 ? ovl_free : &acc_empty[b]));
+          const float* bs = bias_s + 128 * h;
+          const int valid = N - (n0 + 128 * h);  // columns of the block below N
+          float a = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 128; j += 16) {
+#pragma unroll
+            for (int e = j; e < j + 16; ++e) v[e] += bs[e];
+            gelu_n<16>(v + j);
+            if (valid < 128) {
+#pragma unroll
+              for (int e = j; e < j + 16; ++e) v[e] = e < valid ? v[e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = j; e < j + 16; ++e) a = fmaxf(a, fabsf(v[e]));
+          }
+          const uint32_t sb = fp8_scale_byte(a);
+          sbytes |= sb << (8 * h);
+          const float inv = fp8_inv_scale(sb);
+          if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // 16-byte chunk j = columns 16 j .. 16 j + 15
+            const float* c = v + 16 * j;
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(cvt_e4m3x4(c[0] * inv, c[1] * inv, c[2] * inv, c[3] * inv),
+                           cvt_e4m3x4(c[4] * inv, c[5] * inv, c[6] * inv, c[7] * inv),
+                           cvt_e4m3x4(c[8] * inv, c[9] * inv, c[10] * inv, c[11] * inv),
+                           cvt_e4m3x4(c[12] * inv, c[13] * inv, c[14] * inv, c[15] * inv));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && valid > 0 && m0 + 32 * q < p.M) {
+            tma_store_2d(&tm_y, smem_u32(blk), n0 + 128 * h, m0 + 32 * q);
+            bulk_commit_group();
+          }
+        }
+        // the row's two scale bytes: half of a word of four blocks; the last
+        // tile of an odd number writes the word's other half as zeros too.
+        // Padding rows of the last 128-row band get zeros.
+        const int m = m0 + 32 * q + lane;
+        if (m0 < p.M) {
+          if (m >= p.M) sbytes = 0;
+          const int64_t y_tiles = fp8_band_tiles(N);
+          uint8_t* dst = p.y_scales + fp8_scale_offset(m, n0 >> 7, y_tiles);
+          if (((n0 >> 8) & 1) == 0 && n0 + kL8BN >= N) *reinterpret_cast<uint32_t*>(dst) = sbytes;
+          else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sbytes);
+        }
+      } else {
+#pragma unroll 1
+        for (int gi = 0; gi < 4; ++gi) {
+          // 64-column groups; the 64 shared columns ([192, 256)) come first
+          const int c0 = b ? 2 * gi : ((6 + 2 * gi) & 7);  // first 32-column chunk
+          uint32_t v[64];
+          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * c0, v);
+          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * c0 + 32, v + 32);
+          tmem_ld_wait();
+          if (gi == 0 || gi == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead(gi == 0 ? ovl_free : &acc_empty[b]));
+          }
+          if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
+          __syncwarp();
+          const float* bs = bias_s + 32 * c0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // 16-byte chunk j = columns 8 j .. 8 j + 7
+            auto y = [&](int e) { return __uint_as_float(v[8 * j + e]) + bs[8 * j + e]; };
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(y(0), y(1)), pack_bf16x2(y(2), y(3)), pack_bf16x2(y(4), y(5)),
+                           pack_bf16x2(y(6), y(7)));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n0 + 32 * c0 < N && m0 + 32 * q < p.M) {
+            tma_store_2d(&tm_y, smem_u32(blk), n0 + 32 * c0, m0 + 32 * q);
+            bulk_commit_group();
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();  // stores complete before the CTA exits
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's MMAs are complete before either CTA frees TMEM
+  if (warp == 1) tmem_dealloc_pair(tmem, kL8TmemCols);
+}
+
+}  // namespace svdq

@@ -310,6 +310,27 @@ __device__ __forceinline__ void e_mma_nvf4(uint32_t d_tmem, uint64_t adesc, uint
                : "memory");
 }
 
+// One CTA's block-scaled FP8 MMA (E4M3 operands, K = 32, one UE8M0 scale per
+// 32 along K read from tmem; the byte of each scale word is chosen by idesc).
+__device__ __forceinline__ void e_mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(SVDQ_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;" SVDQ_ELECT_END ::
+                   "r"(d_tmem),
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+               : "memory");
+}
+
+// The same across the CTA pair.
+__device__ __forceinline__ void e_mma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(SVDQ_ELECT_BEGIN ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;" SVDQ_ELECT_END ::
+                   "r"(d_tmem),
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+               : "memory");
+}
+
 // Arrive once on this CTA's mbarrier when all prior tcgen05 ops of this
 // thread are complete.
 __device__ __forceinline__ void e_commit(uint32_t bar) {

@@ -15,7 +15,9 @@
 
 #include "../../include/svdq.h"
 #include "calib.cuh"
+#include "fp8.cuh"
 #include "linear.cuh"
+#include "linear_fp8.cuh"
 #include "linear_splitk.cuh"
 #include "lora.cuh"
 #include "pack_residual.cuh"
@@ -28,6 +30,8 @@ namespace {
 // count and 32-bit index product of the kernels in range.
 constexpr int64_t kMaxRows = int64_t(1) << 22;
 constexpr int64_t kMaxK = int64_t(1) << 20;
+// svdq_rmsnorm keeps a row in one CTA's registers: 1024 threads x 4 x 8 values.
+constexpr int64_t kMaxNormK = 32768;
 
 // Which linear kernel svdq_linear launches: 0 picks by shape, 1 forces the
 // large-M kernel, 2 the small-M kernel (svdq_set_linear_path).
@@ -300,6 +304,110 @@ svdq_status launch_linear_splitk(const CUtensorMap& tm_xc, const CUtensorMap& tm
   return launch_status();
 }
 
+// ------------------------------------------------------------ 8-bit layer --
+// Launches `kern` with the layer's launch-overlap setting.
+template <typename... P, typename... A>
+svdq_status launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, void* stream,
+                   A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  unsigned na = 0;
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    na = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = add_overlap_attr(attr, na);
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) != cudaSuccess) return SVDQ_ERR_CUDA;
+  return launch_status();
+}
+
+// Codes [rows][K] as boxes of 128 columns x `box_rows` rows, 128-byte swizzle.
+svdq_status fp8_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, uint32_t box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(K)};
+  const uint32_t box[2] = {128, box_rows};
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Scale tiles of 512 bytes, viewed as [tiles][2][256]: one tile a box.
+svdq_status fp8_scales_map(CUtensorMap* map, const void* scales, int64_t rows, int64_t K) {
+  const uint64_t dims[3] = {256, 2,
+                            static_cast<uint64_t>((rows + 127) / 128) * static_cast<uint64_t>(svdq::fp8_band_tiles(K))};
+  const uint64_t strides[2] = {256, 512};
+  const uint32_t box[3] = {256, 2, 1};
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The product's entry: Y bf16 [M][N] (y_scales null), or codes [M][N] with
+// y_scales and the GELU epilogue.
+svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                            const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
+                            uint8_t* y_scales, bool fp8_out, void* stream) {
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !Y || (fp8_out && !y_scales) || M <= 0 || K <= 0 || N <= 0)
+    return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % (fp8_out ? 16 : 8) != 0 || M > kMaxRows || N > kMaxRows || K > kMaxK ||
+      (fp8_out && N > kMaxK))
+    return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y) ||
+      (bias && !aligned16(bias)) || (y_scales && !aligned16(y_scales)))
+    return SVDQ_ERR_MISALIGNED;
+  const int dev = current_device();
+  if (dev < 0) return SVDQ_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms < 2) return SVDQ_ERR_CUDA;
+
+  CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y;
+  if (svdq_status rc = fp8_codes_map(&tm_x, x_codes, M, K, 128)) return rc;
+  if (svdq_status rc = fp8_codes_map(&tm_w, w_codes, N, K, 128)) return rc;
+  if (svdq_status rc = fp8_scales_map(&tm_xs, x_scales, M, K)) return rc;
+  if (svdq_status rc = fp8_scales_map(&tm_ws, w_scales, N, K)) return rc;
+  if (fp8_out) {
+    if (svdq_status rc = fp8_codes_map(&tm_y, Y, M, N, 32)) return rc;  // one epilogue warp's 32 x 128 block
+  } else {
+    const uint64_t dims[2] = {static_cast<uint64_t>(N), static_cast<uint64_t>(M)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(N) * 2};
+    const uint32_t box[2] = {64, 32};  // one epilogue warp's 32 x 64 block
+    if (svdq_status rc = make_tmap(&tm_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, dims, strides, box,
+                                   CU_TENSOR_MAP_SWIZZLE_128B))
+      return rc;
+  }
+  svdq::L8Params p;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.y_scales = y_scales;
+  p.M = static_cast<int>(M);
+  p.K = static_cast<int>(K);
+  p.N = static_cast<int>(N);
+  p.m_tiles = static_cast<int>((M + svdq::kL8BM - 1) / svdq::kL8BM);
+  p.tiles = p.m_tiles * static_cast<int>((N + svdq::kL8BN - 1) / svdq::kL8BN);
+  p.timeout_ns = wait_timeout_ns();
+  const size_t smem = 1024 + svdq::kL8BarOffset + (svdq::kL8NumBars + 4) * 8;
+  auto kern = fp8_out ? svdq::linear_fp8_kernel<true> : svdq::linear_fp8_kernel<false>;
+  if (svdq_status rc = ensure_smem(reinterpret_cast<const void*>(kern), dev, smem)) return rc;
+  const int pairs = p.tiles < sms / 2 ? p.tiles : sms / 2;
+  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), svdq::kL8Threads, smem, 2, stream, tm_x, tm_w, tm_xs,
+                tm_ws, tm_y, p);
+}
+
+template <typename RES>
+svdq_status launch_rmsnorm(const void* X, int64_t ldx, const void* residual, const void* gamma, float eps, int64_t M,
+                           int64_t K, void* residual_out, void* Y, uint8_t* x_codes, uint8_t* x_scales, void* stream) {
+  const int64_t chunks = K / 8;
+  const int v = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
+  const unsigned threads = static_cast<unsigned>(((chunks + v - 1) / v + 31) / 32 * 32);
+  auto kern = v == 1 ? svdq::rmsnorm_kernel<1, RES> : v == 2 ? svdq::rmsnorm_kernel<2, RES> : svdq::rmsnorm_kernel<4, RES>;
+  return launch(kern, dim3(static_cast<unsigned>(M + 1)), threads, 0, 1, stream, static_cast<const __nv_bfloat16*>(X),
+                ldx, static_cast<const RES*>(residual), static_cast<const __nv_bfloat16*>(gamma), eps,
+                static_cast<int>(M), static_cast<int>(K), static_cast<RES*>(residual_out),
+                static_cast<__nv_bfloat16*>(Y), x_codes, x_scales);
+}
 }  // namespace
 
 extern "C" {
@@ -611,6 +719,73 @@ svdq_status svdq_linear_scaled(const uint8_t* x_codes, const uint8_t* x_scales, 
   if (cudaLaunchKernelEx(&cfg, kern, tm_xc, tm_rc, tm_xs, tm_rs, tm_t, tm_l2, tm_y, p) != cudaSuccess)
     return SVDQ_ERR_CUDA;
   return launch_status();
+}
+
+// ------------------------------------------------------------- 8-bit layer --
+
+svdq_status svdq_fp8_sizes(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes) {
+  if (rows < 0 || K <= 0 || !codes_bytes || !scales_bytes) return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > kMaxK || rows > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  *codes_bytes = static_cast<size_t>(rows) * static_cast<size_t>(K);
+  *scales_bytes = static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(svdq::fp8_band_tiles(K)) * 512;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_pack_weight_fp8(const void* W, int w_dtype, int64_t K, int64_t N, uint8_t* w_codes,
+                                 uint8_t* w_scales, void* stream) {
+  if (!W || !w_codes || !w_scales || K <= 0 || N <= 0 || (w_dtype != SVDQ_BF16 && w_dtype != SVDQ_F32))
+    return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % 8 != 0 || K > kMaxK || N > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(W) || !aligned16(w_codes) || !aligned16(w_scales)) return SVDQ_ERR_MISALIGNED;
+  const dim3 grid(static_cast<unsigned>((N + 127) / 128 * (128 / svdq::kPw8N)),
+                  static_cast<unsigned>(4 * svdq::fp8_band_tiles(K)));
+  if (w_dtype == SVDQ_BF16)
+    return launch(svdq::pack_weight_fp8_kernel<__nv_bfloat16>, grid, svdq::kPw8Threads, 0, 1, stream,
+                  static_cast<const __nv_bfloat16*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
+  return launch(svdq::pack_weight_fp8_kernel<float>, grid, svdq::kPw8Threads, 0, 1, stream,
+                static_cast<const float*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
+}
+
+svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, int gelu, uint8_t* x_codes,
+                              uint8_t* x_scales, void* stream) {
+  if (!X || !x_codes || !x_scales || M <= 0 || K <= 0 || ldx < K || (gelu != 0 && gelu != 1))
+    return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || ldx % 8 != 0 || M > kMaxRows || K > kMaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(X) || !aligned16(x_codes) || !aligned16(x_scales)) return SVDQ_ERR_MISALIGNED;
+  const dim3 grid(static_cast<unsigned>((M + svdq::kQ8Rows - 1) / svdq::kQ8Rows + 1),
+                  static_cast<unsigned>((64 * svdq::fp8_band_tiles(K) + svdq::kQ8Threads - 1) / svdq::kQ8Threads));
+  return launch(gelu ? svdq::quantize_fp8_kernel<true> : svdq::quantize_fp8_kernel<false>, grid, svdq::kQ8Threads, 0, 1,
+                stream, static_cast<const __nv_bfloat16*>(X), ldx, static_cast<int>(M), static_cast<int>(K), x_codes,
+                x_scales);
+}
+
+svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int residual_dtype, const void* gamma,
+                         float eps, int64_t M, int64_t K, void* residual_out, void* Y, uint8_t* x_codes,
+                         uint8_t* x_scales, void* stream) {
+  if (!X || M <= 0 || K <= 0 || ldx < K || !(eps >= 0.0f) || !std::isfinite(eps) ||
+      (residual_dtype != SVDQ_BF16 && residual_dtype != SVDQ_F32))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!residual != !residual_out || !x_codes != !x_scales || (!Y && !x_codes)) return SVDQ_ERR_INVALID_ARG;
+  if (K % 16 != 0 || ldx % 8 != 0 || M > kMaxRows || K > kMaxNormK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+  for (const void* q : {X, residual, gamma, static_cast<const void*>(residual_out), static_cast<const void*>(Y),
+                        static_cast<const void*>(x_codes), static_cast<const void*>(x_scales)})
+    if (!aligned16(q)) return SVDQ_ERR_MISALIGNED;
+  return residual_dtype == SVDQ_F32
+             ? launch_rmsnorm<float>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales, stream)
+             : launch_rmsnorm<__nv_bfloat16>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales,
+                                             stream);
+}
+
+svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                            const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
+                            void* stream) {
+  return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, false, stream);
+}
+
+svdq_status svdq_linear_fp8_gelu(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                                 const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N,
+                                 uint8_t* y_codes, uint8_t* y_scales, void* stream) {
+  return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, y_codes, y_scales, true, stream);
 }
 
 svdq_status svdq_attach_lora(const void* L1, const void* L2, const float* lambda, const void* A, const void* B,

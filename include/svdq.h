@@ -222,6 +222,106 @@ svdq_status svdq_attach_lora(const void* L1, const void* L2, const float* lambda
  */
 svdq_status svdq_channel_absmax(const void* X, int64_t M, int64_t K, float* amax, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit layer.  SVDQuant quantises a layer to 4 bits; a layer that 4 bits
+ * damage (the pages' MixDQ article keeps sensitive layers at 8 bits) can
+ * keep 8: weights and activations in the "FP8 block-128" format below,
+ * multiplied on the same tensor cores at twice the 16-bit rate, with the
+ * norm, the residual's addition, the GELU and the quantisers fused into
+ * their neighbours.  An MLP between two layers is three launches:
+ *     svdq_rmsnorm -> svdq_linear_fp8_gelu -> svdq_linear_fp8.
+ *
+ * FP8 block-128
+ *  - codes: uint8 E4M3 [rows][K];
+ *  - scales: uint8 E8M0 (byte b stands for 2^(b - 127)), one per 128
+ *    consecutive elements along K (the last block of a row may be shorter),
+ *    in the tile layout of the 4-bit scales: rows padded to a multiple of
+ *    128, blocks to a multiple of 4; tile (row / 128, blk / 4) is 512
+ *    contiguous bytes, a band's tiles consecutive along K, (row, blk) at
+ *    byte (row % 32) * 16 + ((row % 128) / 32) * 4 + (blk % 4).  Scales of
+ *    padding rows and blocks are written as 0.
+ *  - a block with amax = max |v_i| takes the smallest 2^e, e >= -127, with
+ *    amax <= 448 2^e, and the codes E4M3_RNE(v_i 2^-e); the division by a
+ *    power of two is exact and nothing saturates.  A NaN becomes the code
+ *    NaN and does not change its block's scale; an infinity becomes
+ *    +-448 2^120.
+ * Conventions as above, with these sizes: K a multiple of 16, N a multiple of
+ * 8 (16 for svdq_linear_fp8_gelu), M >= 1.  No call needs a workspace, and
+ * equal inputs give equal bits. */
+typedef enum { SVDQ_BF16 = 0, SVDQ_F32 = 1 } svdq_dtype;
+
+/* Bytes of the FP8 block-128 buffers for `rows` vectors of length K:
+ * codes_bytes = rows * K, scales_bytes = ceil(rows / 128) * ceil(K / 512) *
+ * 512.  Host-only. */
+svdq_status svdq_fp8_sizes(int64_t rows, int64_t K, size_t* codes_bytes, size_t* scales_bytes);
+
+/*
+ * Weight packer, run once per weight.
+ *   W         [K][N] bf16 or fp32 (w_dtype, an svdq_dtype)
+ *   w_codes   uint8 [N][K]   output: one row per output channel, blocks along K
+ *   w_scales  uint8, svdq_fp8_sizes(N, K) bytes, output
+ */
+svdq_status svdq_pack_weight_fp8(const void* W, int w_dtype, int64_t K, int64_t N, uint8_t* w_codes,
+                                 uint8_t* w_scales, void* stream);
+
+/*
+ * Activation quantiser: X, or GELU(X) with gelu = 1, to FP8 block-128.
+ *   X         bf16 [M][K], row stride ldx elements (ldx >= K, a multiple of
+ *             8: a column range of a wider tensor)
+ *   gelu      0 or 1; GELU(x) = 0.5 x (1 + erf(x / sqrt 2)) in fp32, good to
+ *             about 1e-6 relative also for negative x, not rounded to bf16
+ *             before the quantiser.  (svdq_quantize_act_gelu evaluates the
+ *             same function by an approximation with 3e-7 absolute error.)
+ *             An infinite x gives NaN.
+ *   x_codes   uint8 [M][K] output;   x_scales   svdq_fp8_sizes(M, K) output
+ */
+svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, int gelu, uint8_t* x_codes,
+                              uint8_t* x_scales, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, from one read of each:
+ *     h = X + residual (rounded to the residual's type and stored),
+ *     y = h / sqrt(mean_k(h^2) + eps) * gamma,
+ * y to FP8 block-128 and / or bf16.  The norm is taken of the stored h, so the
+ * result is that of an addition and a norm of their own; sums, root and
+ * products are fp32, each output rounded once.
+ *   X             bf16 [M][K], row stride ldx (ldx >= K, a multiple of 8)
+ *   residual      [M][K] of residual_dtype (an svdq_dtype), or NULL
+ *   gamma         bf16 [K], or NULL for ones
+ *   eps           >= 0, finite
+ *   residual_out  [M][K] of residual_dtype: h (NULL iff residual is); may be
+ *                 `residual` itself
+ *   Y             bf16 [M][K] output or NULL; may be X when ldx == K
+ *   x_codes, x_scales  FP8 block-128 output, both or neither; one of Y and
+ *                 x_codes is needed
+ * K <= 32768.
+ */
+svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int residual_dtype, const void* gamma,
+                         float eps, int64_t M, int64_t K, void* residual_out, void* Y, uint8_t* x_codes,
+                         uint8_t* x_scales, void* stream);
+
+/*
+ * 8-bit linear: Y = deq(x) deq(w)^T + bias as bf16.
+ *   x_codes, x_scales   FP8 block-128 of M rows of length K
+ *   w_codes, w_scales   from svdq_pack_weight_fp8 (N rows)
+ *   bias                bf16 [N] or NULL (added in fp32)
+ *   Y                   bf16 [M][N] output
+ */
+svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                            const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
+                            void* stream);
+
+/*
+ * 8-bit linear whose epilogue is the next layer's activation step:
+ * GELU(deq(x) deq(w)^T + bias), taken in fp32 (GELU as svdq_quantize_fp8), to
+ * FP8 block-128 along N.
+ *   y_codes   uint8 [M][N] output;   y_scales   svdq_fp8_sizes(M, N) output
+ * N a multiple of 16, N <= 2^20.
+ */
+svdq_status svdq_linear_fp8_gelu(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                                 const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N,
+                                 uint8_t* y_codes, uint8_t* y_scales, void* stream);
+
 /*
  * Kernel choice of svdq_linear (host-side setting for the whole process):
  *   0  by shape (default): the small-M kernel (128 x 128 tiles with K split

@@ -1,0 +1,479 @@
+"""The 8-bit layer on the GPU against its 64-bit reference (tests/_fp8_ref.py).
+
+Tolerances, from the arithmetic of each call (u = 2^-24, half an fp32 step):
+- quantise and pack without GELU: none.  Scaling by a power of two is exact.
+- GELU: |error| <= 2^-19 |GELU(x)| for inputs in [-13, 13]: the fit of
+  log2 Phi is within 1.3e-7 in ln Phi, its fp32 evaluation (|g| <= 27, ten
+  fused steps) adds up to about 8e-7, the exponential 2 u, the last product u.
+- norm: the sum of squares is a chain of at most 32 fused steps, then two
+  five-step trees, so 42 u relative, of which the root takes half; division,
+  addition, root, two products: 5 u more.  26 u < 2^-19.
+- linear: an fp32 accumulation of ceil(K / 32) MMA results, each step off by
+  at most one step of the running sum (2^-23 of the sum of absolute terms E),
+  the bias one more, then half a bf16 step.
+- linear + GELU: the same accumulation error times max |GELU'| < 1.13, then
+  the GELU's own."""
+
+import numpy as np
+import pytest
+
+from tests import _fp8_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+GELU_REL = 2.0 ** -19
+NORM_REL = 2.0 ** -19
+
+
+def _m():
+    import torch
+    import bit_w4a4_quantized_smooth_b200 as svdq
+    return torch, svdq
+
+
+def _np(t):
+    import torch
+    if t.element_size() == 1:
+        return t.view(torch.uint8).cpu().numpy()
+    return t.double().cpu().numpy()
+
+
+def _dev(a, dtype):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda()
+
+
+def _ok():
+    torch, svdq = _m()
+    torch.cuda.synchronize()
+    assert svdq.sync_status() == (0, 0)
+
+
+def _act(rng, M, K):
+    """bf16 activations with large channels, zeros of both signs, an all-zero
+    block and a block of tiny values."""
+    torch, _ = _m()
+    x = rng.normal(size=(M, K))
+    x[:, rng.random(K) < 0.02] *= 60.0
+    x[0, : min(K, 128)] = 0.0
+    x[M // 2, 0] = -0.0
+    x[M - 1, -min(K, 100):] *= 1e-38
+    return torch.from_numpy(x).to(torch.bfloat16).cuda()
+
+
+# --------------------------------------------------------------- quantise --
+SHAPES = [(1, 16), (1, 128), (3, 112), (5, 144), (33, 512), (127, 528), (128, 640), (129, 1040), (300, 2064),
+          (2, 12288)]
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_quantize_bit_exact(M, K):
+    torch, svdq = _m()
+    X = _act(np.random.default_rng(M * 7 + K), M, K)
+    codes, scales = svdq.quantize_fp8(X)
+    _ok()
+    c, s = ref.encode(_np(X))
+    assert np.array_equal(_np(codes), c)
+    assert np.array_equal(_np(scales), ref.tiles(s))
+
+
+def test_quantize_strided_rows_into_given_outputs():
+    """A column range of a wider tensor; outputs of uint8 type, dirty before."""
+    torch, svdq = _m()
+    W = _act(np.random.default_rng(5), 70, 1024)
+    X = W[:, 384:384 + 272]
+    codes = torch.full((70, 272), 0xAA, dtype=torch.uint8, device="cuda")
+    scales = torch.full((512,), 0xAA, dtype=torch.uint8, device="cuda")
+    svdq.quantize_fp8(X, codes, scales)
+    _ok()
+    c, s = ref.encode(_np(X))
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), ref.tiles(s))
+
+
+def test_quantize_special_values():
+    """Every exponent of bf16, E4M3 ties, the scale's borders, NaN and infinity."""
+    torch, svdq = _m()
+    bits = np.arange(0, 0x7F80, 1, dtype=np.int32)            # every finite positive bf16
+    X = torch.from_numpy(bits.astype(np.int16)).view(torch.bfloat16).cuda().view(-1, 128)
+    X = torch.cat([X, -X, X.flip(0) * 1.0])
+    codes, scales = svdq.quantize_fp8(X)
+    _ok()
+    c, s = ref.encode(_np(X))
+    assert np.array_equal(_np(codes), c) and np.array_equal(_np(scales), ref.tiles(s))
+    Y = torch.ones((2, 256), dtype=torch.bfloat16, device="cuda")
+    Y[0, 5], Y[1, 7], Y[1, 200] = float("nan"), float("inf"), float("-inf")
+    codes, scales = svdq.quantize_fp8(Y)
+    _ok()
+    v = codes.float().cpu()
+    s, _ = ref.untile(_np(scales), 2, 256)
+    assert torch.isnan(v[0, 5]) and torch.isnan(v).sum() == 1 and (v[0, 6:] == v[0, 6]).all()
+    assert s[0, 0] == s[0, 1] and s[1, 0] == s[1, 1] == 247 and v[1, 7] == 448 and v[1, 200] == -448
+
+
+@pytest.mark.parametrize("M,K", [(1, 128), (9, 400), (130, 2048)])
+def test_quantize_gelu(M, K):
+    torch, svdq = _m()
+    rng = np.random.default_rng(K)
+    X = _dev(rng.normal(size=(M, K)) * 2.5, torch.bfloat16)
+    X[0, :100] = torch.linspace(-13, 13, 100)
+    codes, scales = svdq.quantize_fp8(X, gelu=True)
+    _ok()
+    g = ref.gelu(_np(X))
+    ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
+
+
+def test_gelu_over_its_range():
+    """Blocks of one sign and size each, so that small results are not hidden by large ones."""
+    torch, svdq = _m()
+    x = np.concatenate([np.linspace(a, b, 128) for a, b in
+                        ((-13, -12), (-9, -8), (-6, -5.2), (-5.6, -5.4), (-4, -3), (-1, -0.5), (-1e-3, 1e-3),
+                         (-1e-30, 1e-30), (0.5, 1), (5.4, 5.6), (8, 9), (100, 1000))])
+    X = _dev(x.reshape(1, -1), torch.bfloat16)
+    codes, scales = svdq.quantize_fp8(X, gelu=True)
+    _ok()
+    g = ref.gelu(_np(X))
+    ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
+
+
+# ------------------------------------------------------------------- pack --
+@pytest.mark.parametrize("K,N", [(16, 8), (64, 16), (128, 128), (144, 136), (520 - 8, 264), (1040, 1000), (2064, 72)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_pack_weight_bit_exact(K, N, dt):
+    torch, svdq = _m()
+    rng = np.random.default_rng(K + N)
+    w = rng.normal(size=(K, N)) * 10.0 ** rng.uniform(-6, 3, (1, N))
+    w[:, 0] = 0.0
+    W = _dev(w, torch.bfloat16 if dt == "bf16" else torch.float32)
+    codes, scales = svdq.pack_weight_fp8(W)
+    _ok()
+    c, s = ref.encode(np.ascontiguousarray(_np(W).T))
+    assert np.array_equal(_np(codes), c) and np.array_equal(_np(scales), ref.tiles(s))
+
+
+# ------------------------------------------------------------------- norm --
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 3072), (2, 128), (5, 144), (129, 528), (64, 4112), (3, 8208), (2, 16384),
+                                 (1, 32768)])
+@pytest.mark.parametrize("res", ["none", "bf16", "f32"])
+@pytest.mark.parametrize("gamma", [True, False])
+def test_rmsnorm(M, K, res, gamma):
+    torch, svdq = _m()
+    rng = np.random.default_rng(M + K)
+    X = _act(rng, M, K)
+    R = None if res == "none" else _dev(rng.normal(size=(M, K)) * 3, torch.float32 if res == "f32" else torch.bfloat16)
+    G = _dev(1 + 0.2 * rng.normal(size=K), torch.bfloat16) if gamma else None
+    eps = 1e-5
+    codes, scales, out, Y = svdq.rmsnorm(X, G, R, eps=eps, bf16_out=True)
+    _ok()
+    if R is None:
+        assert out is None
+        h = _np(X)
+    else:
+        assert torch.equal(out, (X.float() + R.float()).to(R.dtype))
+        h = _np(out)
+    y = h / np.sqrt((h * h).mean(axis=1, keepdims=True) + eps)
+    if gamma:
+        y = y * _np(G)
+    err = np.abs(y) * NORM_REL
+    ref.assert_encodes(_np(codes), _np(scales), y, err)
+    got = _np(Y)
+    ok = np.abs(y) > 1e-30
+    assert (got[ok] >= ref.bf16_round(y - err)[ok]).all() and (got[ok] <= ref.bf16_round(y + err)[ok]).all()
+    assert np.abs(got[~ok]).max(initial=0.0) <= 1.01e-30
+
+
+def test_rmsnorm_in_place_strided_and_partial_outputs():
+    """The residual stream updated in place, X a column range, one output only."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(11)
+    W = _act(rng, 40, 2048)
+    X = W[:, 512:512 + 1040]
+    R = _dev(rng.normal(size=(40, 1040)), torch.bfloat16)
+    G = _dev(1 + 0.1 * rng.normal(size=1040), torch.bfloat16)
+    a = svdq.rmsnorm(X, G, R, bf16_out=True)
+    Xc = X.contiguous()
+    b = svdq.rmsnorm(Xc, G, R, fp8_out=False, Y=Xc)            # Y over X
+    assert b[0] is None and b[1] is None and torch.equal(b[3], a[3]) and torch.equal(b[2], a[2])
+    R2 = R.clone()
+    c = svdq.rmsnorm(X, G, R2, residual_out=R2)                # in place
+    _ok()
+    assert c[2] is R2 and torch.equal(R2, a[2]) and c[3] is None
+    assert torch.equal(c[0].view(torch.uint8), a[0].view(torch.uint8))
+    assert torch.equal(c[1].view(torch.uint8), a[1].view(torch.uint8))
+
+
+def test_rmsnorm_rows_of_zeros_and_of_huge_values():
+    """A zero row divides by sqrt(eps) alone (eps 0: 0 / 0 is NaN); a row whose
+    squares leave the fp32 range gives zeros, a NaN stays in its row."""
+    torch, svdq = _m()
+    X = torch.ones((4, 256), dtype=torch.bfloat16, device="cuda")
+    X[0] = 0.0
+    X[1] = 3e38
+    X[2, 3] = float("nan")
+    codes, scales, _, Y = svdq.rmsnorm(X, bf16_out=True)
+    _ok()
+    v = codes.float()
+    assert (v[0] == 0).all() and (Y[0] == 0).all()
+    assert (v[1] == 0).all()
+    assert torch.isnan(v[2]).all() and not torch.isnan(v[3]).any() and (Y[3] == 1).all()
+
+
+# ----------------------------------------------------------------- linear --
+LINEAR = [(1, 16, 8), (1, 128, 16), (2, 144, 136), (3, 528, 248), (8, 1024, 256), (9, 640, 264), (16, 2064, 520),
+          (31, 512, 72), (64, 3200, 384), (127, 1168, 512), (128, 512, 128), (129, 1040, 264), (255, 400, 304),
+          (256, 1024, 512), (257, 912, 776), (300, 112, 1032), (600, 1552, 1288), (5, 12288, 320), (130, 12288, 256)]
+
+
+def _layer(rng, M, K, N, bias, fine=False):
+    """Operands of one product as tensors and as fp64 values: x with large
+    channels, a zero row, w with a zero row; blocks of very different scales."""
+    torch, svdq = _m()
+    x = rng.normal(size=(M, K))
+    x[:, rng.random(K) < 0.02] *= 40.0
+    x[M // 2] = 0.0
+    w = rng.normal(size=(N, K)) / np.sqrt(K) * 2.0 ** rng.integers(-3, 4, (N, 1))
+    w[N // 3] = 0.0
+    (xc, xs), (wc, ws) = ref.encode(x), ref.encode(w)
+    b = rng.normal(size=N) * 0.3
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    t = lambda a, d: torch.from_numpy(a).cuda().view(d)
+    ten = (t(xc, f8), t(ref.tiles(xs), e8), t(wc, f8), t(ref.tiles(ws), e8), _dev(b, torch.bfloat16) if bias else None)
+    xv, wv = ref.decode(xc, xs), ref.decode(wc, ws)
+    y = xv @ wv.T
+    E = np.abs(xv) @ np.abs(wv).T
+    if bias:
+        y = y + _np(ten[4])
+        E = E + np.abs(_np(ten[4]))
+    return ten, y, (-(-K // 32) + 1) * 2.0 ** -23 * E
+
+
+def _check_y(Y, y, acc):
+    got = _np(Y)
+    big = np.maximum(np.abs(got), np.abs(y)).astype(np.float32)
+    half = np.spacing(big).astype(np.float64) * 65536.0 / 2.0
+    bad = np.abs(got - y) > half + acc + 1e-38
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[0], got[bad][0], y[bad][0])
+
+
+@pytest.mark.parametrize("M,K,N", LINEAR)
+@pytest.mark.parametrize("bias", [True, False])
+def test_linear(M, K, N, bias):
+    torch, svdq = _m()
+    ten, y, acc = _layer(np.random.default_rng(M + K + N), M, K, N, bias)
+    guard = torch.full(((M + 2), N), 7.0, dtype=torch.bfloat16, device="cuda")
+    Y = svdq.linear_fp8(*ten, Y=guard[1:M + 1])
+    _ok()
+    _check_y(Y, y, acc)
+    assert (guard[0] == 7).all() and (guard[M + 1] == 7).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(M, K, (N + 15) // 16 * 16) for M, K, N in LINEAR])
+@pytest.mark.parametrize("bias", [True, False])
+def test_linear_gelu(M, K, N, bias):
+    torch, svdq = _m()
+    ten, y, acc = _layer(np.random.default_rng(M + K + N), M, K, N, bias)
+    codes = torch.full((M + 2, N), 0x55, dtype=torch.uint8, device="cuda")
+    scales = torch.full((svdq.fp8_sizes(M, N)[1] + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    svdq.linear_fp8_gelu(*ten, y_codes=codes[1:M + 1], y_scales=scales[:-64])
+    _ok()
+    g = ref.gelu(y)
+    ref.assert_encodes(codes[1:M + 1].cpu().numpy(), scales[:-64].cpu().numpy(), g, 1.13 * acc + np.abs(g) * GELU_REL)
+    assert (codes[0] == 0x55).all() and (codes[M + 1] == 0x55).all() and (scales[-64:] == 0x55).all()
+
+
+@pytest.mark.parametrize("K", [272, 1552])
+def test_linear_many_tiles(K):
+    """More than two output tiles for each CTA pair: both accumulators reused."""
+    torch, svdq = _m()
+    M, N = 6000, 2064
+    ten, y, acc = _layer(np.random.default_rng(K), M, K, N, True)
+    _check_y(svdq.linear_fp8(*ten), y, acc)
+    codes, scales = svdq.linear_fp8_gelu(*ten)
+    _ok()
+    rows = np.concatenate([np.arange(0, M, 9), np.arange(M - 40, M)])
+    s, rest = ref.untile(_np(scales), M, N)
+    assert not _np(scales)[rest].any()
+    g = ref.gelu(y[rows])
+    ref.assert_encodes(_np(codes)[rows], ref.tiles(s[rows]), g, 1.13 * acc[rows] + np.abs(g) * GELU_REL)
+
+
+def test_linear_nan_stays_in_its_row():
+    torch, svdq = _m()
+    for M in (4, 200):
+        ten, y, acc = _layer(np.random.default_rng(M), M, 640, 264, False)
+        xc = ten[0].view(torch.uint8).clone()
+        xc[3, 500] = 0x7F
+        Y = svdq.linear_fp8(xc, *ten[1:])
+        _ok()
+        assert torch.isnan(Y[3]).sum() >= 263                  # the zero row of w: NaN * 0 is NaN too
+        assert not torch.isnan(Y[:3]).any() and not torch.isnan(Y[4:]).any()
+
+
+def test_linear_same_bits_again():
+    torch, svdq = _m()
+    for M, K, N in ((5, 4096, 520), (70, 4096, 384), (300, 2064, 776)):
+        ten, _, _ = _layer(np.random.default_rng(M), M, K, N, True)
+        a = svdq.linear_fp8(*ten)
+        for _ in range(3):
+            assert torch.equal(a, svdq.linear_fp8(*ten))
+    _ok()
+
+
+# ----------------------------------------------------- as they are used --
+def _mlp(svdq, L, X, R):
+    """norm -> up + GELU -> down, the residual stream updated in place."""
+    xc, xs, R, _ = svdq.rmsnorm(X, L["gamma"], R, residual_out=R)
+    hc, hs = svdq.linear_fp8_gelu(xc, xs, L["uc"], L["us"], L["ub"])
+    return svdq.linear_fp8(hc, hs, L["dc"], L["ds"], L["db"])
+
+
+def _mlp_weights(svdq, torch, rng, D, H):
+    bf = torch.bfloat16
+    uc, us = svdq.pack_weight_fp8(_dev(rng.normal(size=(D, H)) / np.sqrt(D), bf))
+    dc, ds = svdq.pack_weight_fp8(_dev(rng.normal(size=(H, D)) / np.sqrt(H), torch.float32))
+    return dict(gamma=_dev(1 + 0.1 * rng.normal(size=D), bf), uc=uc, us=us, ub=_dev(rng.normal(size=H) * 0.1, bf),
+                dc=dc, ds=ds, db=_dev(rng.normal(size=D) * 0.1, bf))
+
+
+@pytest.mark.parametrize("M", [1, 7, 48, 200])
+def test_mlp_chain(M):
+    """Two blocks in a row against the same chain in 64 bits, each step on what
+    the step before really gave; then against the unfused calls, bit for bit."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(M)
+    D, H = 512, 1424
+    L = _mlp_weights(svdq, torch, rng, D, H)
+    X = _dev(rng.normal(size=(M, D)), torch.bfloat16)
+    R = _dev(rng.normal(size=(M, D)), torch.float32)
+    R1 = R.clone()
+    Y = _mlp(svdq, L, X, R1)
+    Y2 = _mlp(svdq, L, Y, R1)
+    _ok()
+    Rr = R.clone()
+    for x, want in ((X, Y), (Y, Y2)):
+        xc, xs, Rr, Yb = svdq.rmsnorm(x, L["gamma"], Rr, bf16_out=True)
+        hc, hs = svdq.linear_fp8_gelu(xc, xs, L["uc"], L["us"], L["ub"])
+        got = svdq.linear_fp8(hc, hs, L["dc"], L["ds"], L["db"])
+        assert torch.equal(got, want)
+        s, _ = ref.untile(_np(hs), M, H)
+        ws, _ = ref.untile(_np(L["ds"]), D, H)
+        hv, wv = ref.decode(_np(hc), s), ref.decode(_np(L["dc"]), ws)
+        acc = (-(-H // 32) + 1) * 2.0 ** -23 * (np.abs(hv) @ np.abs(wv).T + np.abs(_np(L["db"])))
+        _check_y(got, hv @ wv.T + _np(L["db"]), acc)
+    assert torch.equal(R1, Rr)
+    _ok()
+
+
+def test_mlp_chain_on_streams_and_in_graphs():
+    """The chain on a side stream, two chains at once, and captured twice with
+    replays interleaved: the same bits as on the default stream."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(3)
+    D, H = 512, 1040
+    L = _mlp_weights(svdq, torch, rng, D, H)
+    Xs = [_dev(rng.normal(size=(m, D)), torch.bfloat16) for m in (4, 150)]
+    Rs = [_dev(rng.normal(size=(m, D)), torch.bfloat16) for m in (4, 150)]
+    want = [_mlp(svdq, L, x, r.clone()) for x, r in zip(Xs, Rs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    for _ in range(3):
+        got = []
+        for st, x, r in zip(streams, Xs, Rs):
+            with torch.cuda.stream(st):
+                got.append(_mlp(svdq, L, x, r.clone()))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs, res = [], [], []
+    for x, r in zip(Xs, Rs):
+        rr = r.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = _mlp(svdq, L, x, rr)
+        graphs.append(g)
+        outs.append(y)
+        res.append(rr)
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                res[i].copy_(Rs[i])
+                outs[i].fill_(float("nan"))
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    _ok()
+    # the stream argument, with the current stream another one
+    st = torch.cuda.Stream()
+    r = Rs[0].clone()
+    st.wait_stream(torch.cuda.current_stream())
+    xc, xs, _, _ = svdq.rmsnorm(Xs[0], L["gamma"], r, residual_out=r, stream=st)
+    hc, hs = svdq.linear_fp8_gelu(xc, xs, L["uc"], L["us"], L["ub"], stream=st)
+    y = svdq.linear_fp8(hc, hs, L["dc"], L["ds"], L["db"], stream=st)
+    st.synchronize()
+    assert torch.equal(y, want[0])
+
+
+def test_norm_feeds_the_4_bit_layer():
+    """The norm's bf16 output through the 4-bit layer's own calls, beside the FP8
+    output of the same read: the two layers in one block."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(9)
+    M, K, N = 40, 512, 256
+    X = _dev(rng.normal(size=(M, K)), torch.bfloat16)
+    R = _dev(rng.normal(size=(M, K)), torch.bfloat16)
+    w = rng.normal(size=(K, N)) / np.sqrt(K)
+    rc, rs = svdq.pack_residual(_dev(w, torch.float32))
+    wc, ws = svdq.pack_weight_fp8(_dev(w, torch.float32))
+    inv = torch.ones(K, device="cuda")
+    xc, xs, h, Yn = svdq.rmsnorm(X, None, R, bf16_out=True)
+    qc, qs, _ = svdq.quantize_act(Yn, inv, None)
+    y4 = svdq.linear(qc, qs, None, rc, rs, None, None, M, K, N)
+    y8 = svdq.linear_fp8(xc, xs, wc, ws)
+    _ok()
+    hv = _np(h)
+    y = hv / np.sqrt((hv * hv).mean(axis=1, keepdims=True) + 1e-6) @ w
+    rel = lambda t: np.linalg.norm(_np(t) - y) / np.linalg.norm(y)
+    # one rounding of x and one of w to 4 bits (steps of 1/2 to 2 of 6, rms about
+    # 0.1 each) or to E4M3 (rms 2^-4 / sqrt 3 = 0.036 each, at the most)
+    assert rel(y8) < 0.052 and rel(y8) < rel(y4) < 0.3
+    # the FP8 output equals the quantiser's of the unrounded y: within the norm's error of Yn's
+    c2, s2 = svdq.quantize_fp8(Yn)
+    assert (codes_differ := (c2.view(torch.uint8) != xc.view(torch.uint8)).float().mean().item()) < 0.1, codes_differ
+
+
+def test_calls_leave_launch_overlap_off_unchanged():
+    torch, svdq = _m()
+    rng = np.random.default_rng(13)
+    L = _mlp_weights(svdq, torch, rng, 512, 1040)
+    X, R = (_dev(rng.normal(size=(33, 512)), torch.bfloat16) for _ in range(2))
+    a = _mlp(svdq, L, X, R.clone())
+    try:
+        svdq.set_launch_overlap(False)
+        b = _mlp(svdq, L, X, R.clone())
+    finally:
+        svdq.set_launch_overlap(True)
+    _ok()
+    assert torch.equal(a, b)
+
+
+def test_binding_refusals_on_the_device():
+    torch, svdq = _m()
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")
+    xc, xs = svdq.quantize_fp8(z(4, 256))
+    wc, ws = svdq.pack_weight_fp8(z(256, 32))
+    for call in (lambda: svdq.linear_fp8(xc, xs, wc[:, :128], ws), lambda: svdq.linear_fp8(xc, xs[:-1], wc, ws),
+                 lambda: svdq.linear_fp8(xc, xs, wc, ws, z(31)), lambda: svdq.linear_fp8(xc, xs, wc, ws, Y=z(4, 31)),
+                 lambda: svdq.linear_fp8(xc, xs, wc, ws.cpu()), lambda: svdq.linear_fp8(xc.float(), xs, wc, ws),
+                 lambda: svdq.linear_fp8_gelu(xc, xs, wc, ws, y_codes=z(4, 32)),
+                 lambda: svdq.quantize_fp8(z(256, 4).t()), lambda: svdq.quantize_fp8(z(4, 256), x_scales=xs[:-1]),
+                 lambda: svdq.rmsnorm(z(4, 256), z(255)), lambda: svdq.rmsnorm(z(4, 256), z(256), z(3, 256)),
+                 lambda: svdq.rmsnorm(z(4, 256), z(256), z(4, 256), residual_out=z(4, 256, d=torch.float32)),
+                 lambda: svdq.rmsnorm(z(4, 256), residual_out=z(4, 256)),
+                 lambda: svdq.rmsnorm(z(4, 256), z(256), z(4, 512)[:, ::2]),
+                 lambda: svdq.pack_weight_fp8(z(256, 64)[:, :32])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: svdq.quantize_fp8(z(4, 40)), lambda: svdq.quantize_fp8(z(0, 64)),
+                 lambda: svdq.rmsnorm(z(4, 256), fp8_out=False), lambda: svdq.pack_weight_fp8(z(64, 12)),
+                 lambda: svdq.linear_fp8_gelu(xc, xs, wc[:24], svdq.pack_weight_fp8(z(256, 24))[1])):
+        with pytest.raises(svdq.SvdqError):
+            call()
+    _ok()
