@@ -255,62 +255,28 @@ def channel_absmax(X, amax=None, stream=None):
 # ------------------------------------------------------------- 8-bit layer --
 # Tensors of the FP8 block-128 format: codes float8_e4m3fn [rows][K], scales
 # float8_e8m0fnu, flat, in the tile layout of include/svdq.h (uint8 tensors of
-# the same sizes are taken as well).  These calls check types, shapes and
-# devices (ValueError), and run on the device of their first argument, on that
-# device's current stream unless one is given.
+# the same sizes are taken as well).  Types, shapes, strides and devices are
+# checked (ValueError) in the native module _svdq_torch (csrc/torch_calls.cpp),
+# which allocates the outputs that are not given and makes the C ABI's call on
+# the device of the first argument, on that device's current stream unless one
+# is given.
 
-SVDQ_BF16, SVDQ_F32 = 0, 1
-_call_state = None
-
-
-def _state():
-    """(torch, code types, scale types): looked up once."""
-    global _call_state
-    if _call_state is None:
-        import torch
-        _call_state = (torch, (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8))
-    return _call_state
+_ext = None
 
 
-def _need(t, name: str, dtypes, shape, device):
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-
-
-def _rows_of(X, name: str):
-    """(M, K, row stride) of a 2-D bf16 tensor with unit column stride."""
-    torch = _state()[0]
-    if X.dtype != torch.bfloat16 or X.dim() != 2:
-        raise ValueError(f"{name}: expected a 2-D bfloat16 tensor, got {X.dim()}-D {X.dtype}")
-    if not X.is_cuda:
-        raise ValueError(f"{name}: on {X.device}, expected a CUDA device")
-    M, K = X.shape
-    s0, s1 = X.stride()
-    if (s1 != 1 and K > 1) or (M > 1 and s0 < K):
-        raise ValueError(f"{name}: strides {(s0, s1)}, expected ones of rows that do not overlap")
-    return M, K, s0 if M > 1 else K
-
-
-def _run8(what: str, fn, device, stream, *args):
-    """One call on `device`, on `stream` or the device's current stream."""
-    torch = _state()[0]
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream.cuda_stream)
-    if st != SVDQ_OK:
-        raise SvdqError(st, what)
+def _native():
+    """The native torch calls (raises if they have not been built)."""
+    global _ext
+    if _ext is None:
+        load()
+        path = os.path.join(HERE, "_svdq_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m bit_w4a4_quantized_smooth_b200.build`")
+        import torch  # noqa: F401  (its libraries are what the module is linked to)
+        from . import _svdq_torch
+        _svdq_torch.set_error(SvdqError)
+        _ext = _svdq_torch
+    return _ext
 
 
 def fp8_sizes(rows: int, K: int) -> Tuple[int, int]:
@@ -321,44 +287,15 @@ def fp8_sizes(rows: int, K: int) -> Tuple[int, int]:
     return c.value, s.value
 
 
-def _scales_len(rows: int, K: int) -> int:
-    return ((rows + 127) >> 7) * ((K + 511) >> 9) * 512
-
-
-def _fp8_outputs(rows: int, K: int, codes, scales, device, names):
-    torch, code_types, scale_types = _state()
-    if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=device)
-    else:
-        _need(codes, names[0], code_types, (rows, K), device)
-    if scales is None:
-        scales = torch.empty(_scales_len(rows, K), dtype=torch.float8_e8m0fnu, device=device)
-    else:
-        _need(scales, names[1], scale_types, (_scales_len(rows, K),), device)
-    return codes, scales
-
-
 def pack_weight_fp8(W, w_codes=None, w_scales=None, stream=None):
     """W bf16 or fp32 [K][N] -> (w_codes float8_e4m3fn [N][K], w_scales)."""
-    torch = _state()[0]
-    if W.dim() != 2 or not W.is_cuda:
-        raise ValueError(f"W: expected a 2-D CUDA tensor, got {W.dim()}-D on {W.device}")
-    K, N = W.shape
-    _need(W, "W", (torch.bfloat16, torch.float32), (K, N), W.device)
-    w_codes, w_scales = _fp8_outputs(N, K, w_codes, w_scales, W.device, ("w_codes", "w_scales"))
-    _run8("svdq_pack_weight_fp8", load().svdq_pack_weight_fp8, W.device, stream, W.data_ptr(),
-          SVDQ_F32 if W.dtype == torch.float32 else SVDQ_BF16, K, N, w_codes.data_ptr(), w_scales.data_ptr())
-    return w_codes, w_scales
+    return (_ext or _native()).pack_weight_fp8(W, w_codes, w_scales, stream)
 
 
 def quantize_fp8(X, x_codes=None, x_scales=None, stream=None, gelu: bool = False):
     """X bf16 [M][K] (rows may be strided) -> (x_codes float8_e4m3fn [M][K],
     x_scales) of X, or of GELU(X)."""
-    M, K, ldx = _rows_of(X, "X")
-    x_codes, x_scales = _fp8_outputs(M, K, x_codes, x_scales, X.device, ("x_codes", "x_scales"))
-    _run8("svdq_quantize_fp8", load().svdq_quantize_fp8, X.device, stream, X.data_ptr(), ldx, M, K, 1 if gelu else 0,
-          x_codes.data_ptr(), x_scales.data_ptr())
-    return x_codes, x_scales
+    return (_ext or _native()).quantize_fp8(X, x_codes, x_scales, stream, gelu)
 
 
 def rmsnorm(X, gamma=None, residual=None, eps: float = 1e-6, residual_out=None, Y=None, x_codes=None, x_scales=None,
@@ -369,74 +306,20 @@ def rmsnorm(X, gamma=None, residual=None, eps: float = 1e-6, residual_out=None, 
     residual; pass residual_out=residual to update it in place), y as bf16
     (with bf16_out=True or a given Y).  X bf16 [M][K] (rows may be strided),
     gamma bf16 [K]."""
-    torch = _state()[0]
-    M, K, ldx = _rows_of(X, "X")
-    dev = X.device
-    if gamma is not None:
-        _need(gamma, "gamma", (torch.bfloat16,), (K,), dev)
-    rd = SVDQ_BF16
-    if residual is not None:
-        _need(residual, "residual", (torch.bfloat16, torch.float32), (M, K), dev)
-        if residual.dtype == torch.float32:
-            rd = SVDQ_F32
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-        else:
-            _need(residual_out, "residual_out", (residual.dtype,), (M, K), dev)
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    if fp8_out:
-        x_codes, x_scales = _fp8_outputs(M, K, x_codes, x_scales, dev, ("x_codes", "x_scales"))
-    elif x_codes is not None or x_scales is not None:
-        raise ValueError("x_codes or x_scales with fp8_out=False")
-    if Y is not None:
-        _need(Y, "Y", (torch.bfloat16,), (M, K), dev)
-    elif bf16_out:
-        Y = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    _run8("svdq_rmsnorm", load().svdq_rmsnorm, dev, stream, X.data_ptr(), ldx, _ptr(residual), rd, _ptr(gamma), eps, M,
-          K, _ptr(residual_out), _ptr(Y), _ptr(x_codes), _ptr(x_scales))
-    return x_codes, x_scales, residual_out, Y
-
-
-def _linear8_args(x_codes, x_scales, w_codes, w_scales, bias):
-    torch, code_types, scale_types = _state()
-    if x_codes.dim() != 2 or w_codes.dim() != 2 or not x_codes.is_cuda:
-        raise ValueError(f"x_codes, w_codes: expected 2-D CUDA tensors, got {x_codes.dim()}-D on {x_codes.device} and "
-                         f"{w_codes.dim()}-D")
-    M, K = x_codes.shape
-    N = w_codes.shape[0]
-    dev = x_codes.device
-    _need(x_codes, "x_codes", code_types, (M, K), dev)
-    _need(x_scales, "x_scales", scale_types, (_scales_len(M, K),), dev)
-    _need(w_codes, "w_codes", code_types, (N, K), dev)
-    _need(w_scales, "w_scales", scale_types, (_scales_len(N, K),), dev)
-    if bias is not None:
-        _need(bias, "bias", (torch.bfloat16,), (N,), dev)
-    return M, K, N, dev
+    return (_ext or _native()).rmsnorm(X, gamma, residual, eps, residual_out, Y, x_codes, x_scales, fp8_out, bf16_out,
+                                       stream)
 
 
 def linear_fp8(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, stream=None):
     """8-bit linear: x_codes [M][K], w_codes [N][K] with their scales, bias
     bf16 [N] or None -> Y bf16 [M][N]."""
-    torch = _state()[0]
-    M, K, N, dev = _linear8_args(x_codes, x_scales, w_codes, w_scales, bias)
-    if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(Y, "Y", (torch.bfloat16,), (M, N), dev)
-    _run8("svdq_linear_fp8", load().svdq_linear_fp8, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(),
-          w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), M, K, N, Y.data_ptr())
-    return Y
+    return (_ext or _native()).linear_fp8(x_codes, x_scales, w_codes, w_scales, bias, Y, stream)
 
 
 def linear_fp8_gelu(x_codes, x_scales, w_codes, w_scales, bias=None, y_codes=None, y_scales=None, stream=None):
     """8-bit linear with GELU and the next layer's quantiser in its epilogue
     -> (y_codes float8_e4m3fn [M][N], y_scales)."""
-    M, K, N, dev = _linear8_args(x_codes, x_scales, w_codes, w_scales, bias)
-    y_codes, y_scales = _fp8_outputs(M, N, y_codes, y_scales, dev, ("y_codes", "y_scales"))
-    _run8("svdq_linear_fp8_gelu", load().svdq_linear_fp8_gelu, dev, stream, x_codes.data_ptr(), x_scales.data_ptr(),
-          w_codes.data_ptr(), w_scales.data_ptr(), _ptr(bias), M, K, N, y_codes.data_ptr(), y_scales.data_ptr())
-    return y_codes, y_scales
+    return (_ext or _native()).linear_fp8_gelu(x_codes, x_scales, w_codes, w_scales, bias, y_codes, y_scales, stream)
 
 
 def sync_status(stream=None) -> Tuple[int, int]:

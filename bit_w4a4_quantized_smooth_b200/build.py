@@ -1,7 +1,8 @@
-"""Build the sm_100a shared library ``libsvdq.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libsvdq.so`` in-tree with nvcc, and the
+native torch calls ``_svdq_torch.so`` on top of it with the host compiler.
 
-The library is the product: the three C-ABI calls of include/svdq.h and the
-CUDA kernels behind them.  It is compiled for sm_100a only (B200).
+The library is the product: the C-ABI calls of include/svdq.h and the CUDA
+kernels behind them.  It is compiled for sm_100a only (B200).
 """
 
 from __future__ import annotations
@@ -14,8 +15,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
 SOURCES = [os.path.join(CSRC, "svdq.cu")]
+TORCH_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
+TORCH_LIB = os.path.join(HERE, "_svdq_torch.so")
+HEADER = os.path.join(HERE, "..", "include", "svdq.h")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
-    os.path.join(HERE, "..", "include", "svdq.h")]
+    HEADER]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -29,16 +33,38 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _stale(lib: str, deps) -> bool:
+    if not os.path.exists(lib):
+        return True
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libsvdq.so if it is missing or older than its sources."""
-    if not force and os.path.exists(LIB):
-        t = os.path.getmtime(LIB)
-        if all(os.path.getmtime(d) <= t for d in DEPS if os.path.exists(d)):
-            return LIB
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", LIB + ".tmp"] + SOURCES
-    subprocess.check_call(cmd, cwd=CSRC)
-    os.replace(LIB + ".tmp", LIB)
+    """Compile what is missing or older than its sources; the path of libsvdq.so."""
+    if force or _stale(LIB, DEPS):
+        cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-o", LIB + ".tmp"] + SOURCES
+        subprocess.check_call(cmd, cwd=CSRC)
+        os.replace(LIB + ".tmp", LIB)
+    if force or _stale(TORCH_LIB, [TORCH_SOURCE, HEADER]):
+        build_torch_calls()
     return LIB
+
+
+def build_torch_calls() -> str:
+    """_svdq_torch.so: torch's headers, its C++ libraries (found loaded at run
+    time, after `import torch`) and libsvdq.so beside it."""
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    inc = include_paths() + [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    cmd += [f"-I{d}" for d in inc if os.path.isdir(d)]
+    cmd += [TORCH_SOURCE, "-o", TORCH_LIB + ".tmp"] + [f"-L{d}" for d in library_paths()]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-L{HERE}", "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN"]
+    subprocess.check_call(cmd, cwd=CSRC)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    return TORCH_LIB
 
 
 if __name__ == "__main__":
