@@ -79,6 +79,8 @@ def load() -> ctypes.CDLL:
         L.svdq_channel_absmax.argtypes = [_P, _I64, _I64, _P, _P]
         L.svdq_fp8_sizes.restype = ctypes.c_int
         L.svdq_fp8_sizes.argtypes = [_I64, _I64, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
+        L.svdq_set_linear_fp8_path.restype = ctypes.c_int
+        L.svdq_set_linear_fp8_path.argtypes = [ctypes.c_int]
         L.svdq_pack_weight_fp8.restype = ctypes.c_int
         L.svdq_pack_weight_fp8.argtypes = [_P, ctypes.c_int, _I64, _I64, _P, _P, _P]
         L.svdq_quantize_fp8.restype = ctypes.c_int
@@ -340,6 +342,11 @@ LINEAR_PATHS = {"auto": 0, "large": 1, "small": 2}
 def set_linear_path(path: str):
     """Force svdq_linear's kernel: "auto" (by shape), "large" or "small"."""
     _check(load().svdq_set_linear_path(LINEAR_PATHS[path]), "svdq_set_linear_path")
+
+
+def set_linear_fp8_path(path: str):
+    """Force the kernel of linear_fp8 and linear_fp8_gelu: "auto", "large" or "small"."""
+    _check(load().svdq_set_linear_fp8_path(LINEAR_PATHS[path]), "svdq_set_linear_fp8_path")
 
 
 def set_launch_overlap(enable: bool):

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -18,6 +19,7 @@
 #include "fp8.cuh"
 #include "linear.cuh"
 #include "linear_fp8.cuh"
+#include "linear_fp8_splitk.cuh"
 #include "linear_splitk.cuh"
 #include "lora.cuh"
 #include "pack_residual.cuh"
@@ -36,6 +38,9 @@ constexpr int64_t kMaxNormK = 32768;
 // Which linear kernel svdq_linear launches: 0 picks by shape, 1 forces the
 // large-M kernel, 2 the small-M kernel (svdq_set_linear_path).
 std::atomic<int> g_linear_path{0};
+
+// The same for svdq_linear_fp8 and svdq_linear_fp8_gelu (svdq_set_linear_fp8_path).
+std::atomic<int> g_linear8_path{0};
 
 // Whether the layer's launches carry the programmatic stream-serialisation
 // attribute (svdq_set_launch_overlap; default on).  With it a layer kernel
@@ -346,6 +351,76 @@ svdq_status fp8_scales_map(CUtensorMap* map, const void* scales, int64_t rows, i
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Few rows: 128-channel tiles, K split over a cluster.  `bm` tokens a tile
+// (M padded to 16, at most 128).
+struct S8Plan {
+  int bm, splits, spc, stages;
+  uint32_t tmem_cols;
+  size_t smem;
+};
+
+S8Plan s8_plan(int64_t M, int64_t K, int64_t N, int dev, int sms) {
+  S8Plan pl;
+  pl.bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
+  const int64_t tiles = (N + svdq::kS8BN - 1) / svdq::kS8BN * ((M + svdq::kS8MaxBM - 1) / svdq::kS8MaxBM);
+  const int k_stages = static_cast<int>((K + svdq::kS8BK - 1) / svdq::kS8BK);
+  pl.tmem_cols = pow2_at_least(static_cast<uint32_t>(pl.bm + 32));
+  const uint32_t stage = svdq::s8_stage_bytes(pl.bm);
+  const uint32_t fixed = 1024 + svdq::kS8HeadBytes;
+  // ring depth for two CTAs per SM (half of 227 KB less the reserved bytes)
+  const int depth = std::min<int>(svdq::kS8MaxStages, static_cast<int>((115 * 1024 - fixed) / stage));
+  // the split that gives the busiest SM the fewest stages, with two per CTA
+  // for its start and its reduction; the smaller split on ties
+  int best = 1;
+  int64_t best_cost = -1;
+  for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
+    const int spc = (k_stages + s - 1) / s;
+    if ((k_stages + spc - 1) / spc != s) continue;
+    const int64_t cost = ((tiles * s + sms - 1) / sms) * (spc + 2);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  pl.splits = best;
+  pl.spc = (k_stages + best - 1) / best;
+  pl.stages = std::min(pl.spc, depth);
+  uint32_t ring = static_cast<uint32_t>(pl.stages) * stage;
+  ring = std::max<uint32_t>(ring, static_cast<uint32_t>(pl.bm) * svdq::kS8BN * 4);  // the partials
+  pl.smem = smem_for_tmem(dev, fixed + ring, pl.tmem_cols);
+  return pl;
+}
+
+template <bool FP8_OUT>
+svdq_status launch_s8(const S8Plan& pl, const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                      const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
+                      uint8_t* y_scales, int dev, void* stream) {
+  if (pl.smem == 0 || pl.smem > 232448) return SVDQ_ERR_CUDA;
+  CUtensorMap tm_x, tm_w;
+  if (svdq_status rc = fp8_codes_map(&tm_x, x_codes, M, K, static_cast<uint32_t>(pl.bm))) return rc;
+  if (svdq_status rc = fp8_codes_map(&tm_w, w_codes, N, K, svdq::kS8BN)) return rc;
+  auto kern = svdq::linear_fp8_splitk_kernel<FP8_OUT>;
+  if (svdq_status rc = ensure_smem(reinterpret_cast<const void*>(kern), dev, pl.smem)) return rc;
+  svdq::S8Params p;
+  p.x_scales = x_scales;
+  p.w_scales = w_scales;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.Y = Y;
+  p.y_scales = y_scales;
+  p.M = static_cast<int>(M);
+  p.K = static_cast<int>(K);
+  p.N = static_cast<int>(N);
+  p.bm = pl.bm;
+  p.splits = pl.splits;
+  p.spc = pl.spc;
+  p.stages = pl.stages;
+  p.tmem_cols = pl.tmem_cols;
+  p.timeout_ns = wait_timeout_ns();
+  const dim3 grid(static_cast<unsigned>(pl.splits), static_cast<unsigned>((N + svdq::kS8BN - 1) / svdq::kS8BN),
+                  static_cast<unsigned>((M + svdq::kS8MaxBM - 1) / svdq::kS8MaxBM));
+  return launch(kern, grid, svdq::kS8Threads, pl.smem, static_cast<unsigned>(pl.splits), stream, tm_x, tm_w, p);
+}
+
 // The product's entry: Y bf16 [M][N] (y_scales null), or codes [M][N] with
 // y_scales and the GELU epilogue.
 svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
@@ -363,6 +438,12 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (dev < 0) return SVDQ_ERR_CUDA;
   const int sms = sm_count(dev);
   if (sms < 2) return SVDQ_ERR_CUDA;
+  const int path = g_linear8_path.load(std::memory_order_relaxed);
+  if (path == 2 || (path == 0 && M <= 128)) {
+    const S8Plan pl = s8_plan(M, K, N, dev, sms);
+    return fp8_out ? launch_s8<true>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, dev, stream)
+                   : launch_s8<false>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, dev, stream);
+  }
 
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y;
   if (svdq_status rc = fp8_codes_map(&tm_x, x_codes, M, K, 128)) return rc;
@@ -863,6 +944,12 @@ svdq_status svdq_set_wait_timeout(uint64_t timeout_ns) {
 svdq_status svdq_set_linear_path(int path) {
   if (path < 0 || path > 2) return SVDQ_ERR_INVALID_ARG;
   g_linear_path.store(path, std::memory_order_relaxed);
+  return SVDQ_OK;
+}
+
+svdq_status svdq_set_linear_fp8_path(int path) {
+  if (path < 0 || path > 2) return SVDQ_ERR_INVALID_ARG;
+  g_linear8_path.store(path, std::memory_order_relaxed);
   return SVDQ_OK;
 }
 

@@ -335,6 +335,12 @@ svdq_status svdq_linear_fp8_gelu(const uint8_t* x_codes, const uint8_t* x_scales
  */
 svdq_status svdq_set_linear_path(int path);
 
+/* The same choice for svdq_linear_fp8 and svdq_linear_fp8_gelu: 0 by shape
+ * (default), 1 always the large-M kernel (persistent CTA pairs, 256 x 256
+ * tiles), 2 always the few-rows kernel (128 channels x up to 128 tokens, K
+ * split over a cluster).  Both compute the same sums in another order. */
+svdq_status svdq_set_linear_fp8_path(int path);
+
 /*
  * Launch overlap of the layer calls (host-side setting for the whole
  * process; 1 by default).  With 1, svdq_quantize_act(_gelu, _noalloc) and

@@ -86,6 +86,13 @@ def test_linear_refusals(lib, name):
         assert f(*_bad(ok, i, v)) == status, (i, v)
 
 
+def test_path_setting(lib):
+    from bit_w4a4_quantized_smooth_b200 import set_linear_fp8_path
+    assert lib.svdq_set_linear_fp8_path(3) == 1 and lib.svdq_set_linear_fp8_path(-1) == 1
+    set_linear_fp8_path("small")
+    set_linear_fp8_path("auto")
+
+
 def test_binding_refuses_what_the_abi_cannot_see():
     """Types, shapes, strides and devices are checked before a pointer is taken."""
     import torch

@@ -246,6 +246,15 @@ def _layer(rng, M, K, N, bias, fine=False):
     return ten, y, (-(-K // 32) + 1) * 2.0 ** -23 * E
 
 
+@pytest.fixture(params=["auto", "large", "small"])
+def path(request):
+    """Each test of the product runs by shape, and on both kernels by force."""
+    _, svdq = _m()
+    svdq.set_linear_fp8_path(request.param)
+    yield request.param
+    svdq.set_linear_fp8_path("auto")
+
+
 def _check_y(Y, y, acc):
     got = _np(Y)
     big = np.maximum(np.abs(got), np.abs(y)).astype(np.float32)
@@ -256,7 +265,7 @@ def _check_y(Y, y, acc):
 
 @pytest.mark.parametrize("M,K,N", LINEAR)
 @pytest.mark.parametrize("bias", [True, False])
-def test_linear(M, K, N, bias):
+def test_linear(M, K, N, bias, path):
     torch, svdq = _m()
     ten, y, acc = _layer(np.random.default_rng(M + K + N), M, K, N, bias)
     guard = torch.full(((M + 2), N), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -268,7 +277,7 @@ def test_linear(M, K, N, bias):
 
 @pytest.mark.parametrize("M,K,N", [(M, K, (N + 15) // 16 * 16) for M, K, N in LINEAR])
 @pytest.mark.parametrize("bias", [True, False])
-def test_linear_gelu(M, K, N, bias):
+def test_linear_gelu(M, K, N, bias, path):
     torch, svdq = _m()
     ten, y, acc = _layer(np.random.default_rng(M + K + N), M, K, N, bias)
     codes = torch.full((M + 2, N), 0x55, dtype=torch.uint8, device="cuda")
@@ -296,7 +305,7 @@ def test_linear_many_tiles(K):
     ref.assert_encodes(_np(codes)[rows], ref.tiles(s[rows]), g, 1.13 * acc[rows] + np.abs(g) * GELU_REL)
 
 
-def test_linear_nan_stays_in_its_row():
+def test_linear_nan_stays_in_its_row(path):
     torch, svdq = _m()
     for M in (4, 200):
         ten, y, acc = _layer(np.random.default_rng(M), M, 640, 264, False)
@@ -308,7 +317,7 @@ def test_linear_nan_stays_in_its_row():
         assert not torch.isnan(Y[:3]).any() and not torch.isnan(Y[4:]).any()
 
 
-def test_linear_same_bits_again():
+def test_linear_same_bits_again(path):
     torch, svdq = _m()
     for M, K, N in ((5, 4096, 520), (70, 4096, 384), (300, 2064, 776)):
         ten, _, _ = _layer(np.random.default_rng(M), M, K, N, True)
