@@ -345,7 +345,7 @@ def set_linear_path(path: str):
 
 
 def set_linear_fp8_path(path: str):
-    """Force the kernel of linear_fp8 and linear_fp8_gelu: "auto", "large" or "small"."""
+    """Force the kernel of linear_fp8 and linear_fp8_gelu: "auto" (by shape), "large" or "small"."""
     _check(load().svdq_set_linear_fp8_path(LINEAR_PATHS[path]), "svdq_set_linear_fp8_path")
 
 

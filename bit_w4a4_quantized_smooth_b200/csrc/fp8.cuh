@@ -205,6 +205,36 @@ __device__ __forceinline__ void zero_pad_scales(uint8_t* scales, int64_t M, int6
                                                            band_tiles)) = 0;
 }
 
+// GELU of a token's 128 channels, four per lane of a warp (channel n = this
+// lane's first), as one FP8 block; channels past N count as zeros and are not
+// written.
+__device__ __forceinline__ void store_gelu_fp8(float* v, uint8_t* codes, uint8_t* scales, int64_t m, int n, int N,
+                                               int lane) {
+  gelu_n<4>(v);
+  if (n >= N) v[0] = v[1] = v[2] = v[3] = 0.0f;
+  float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  const uint32_t b = fp8_scale_byte(a);
+  const float inv = fp8_inv_scale(b);
+  if (n < N)
+    *reinterpret_cast<uint32_t*>(codes + m * N + n) = cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  if (lane == 0) scales[fp8_scale_offset(m, n >> 7, fp8_band_tiles(N))] = static_cast<uint8_t>(b);
+}
+
+// Zero scales that the tile of channels [n0, n0 + 128) of the band's rows [m0,
+// m0 + 128) owns: its block of the rows from `rows` on (padding), and, for the
+// last tile, the blocks behind it in the band's last words.
+__device__ __forceinline__ void zero_tile_scales(uint8_t* scales, int rows, int64_t m0, int n0, int N, int tid,
+                                                 int threads) {
+  const int64_t tiles = fp8_band_tiles(N);
+  const int blk = n0 >> 7;
+  for (int r = rows + tid; r < 128; r += threads) scales[fp8_scale_offset(m0 + r, blk, tiles)] = 0;
+  if (n0 + 128 >= N)
+    for (int z = blk + 1; z < 4 * tiles; ++z)
+      for (int r = tid; r < 128; r += threads) scales[fp8_scale_offset(m0 + r, z, tiles)] = 0;
+}
+
 // ============================================================ quantiser ====
 // x codes and scales of X (or GELU(X)), bf16 [M][K] with row stride ldx.
 // Thread = 8 columns of kQ8Rows consecutive rows (one 16-byte load each, all

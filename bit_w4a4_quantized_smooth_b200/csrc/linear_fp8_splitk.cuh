@@ -24,9 +24,9 @@ constexpr int kS8MaxBM = 128;    // tokens per tile at most (MMA N)
 constexpr int kS8BK = 128;
 constexpr uint32_t kS8WBytes = 16384;
 constexpr uint32_t kS8SfBytes = 1024;   // w and x scale tiles of 512 columns
-constexpr int kS8MaxStages = 12;
 constexpr int kS8MaxSplits = 8;
 constexpr uint32_t kS8HeadBytes = 1024;
+constexpr uint32_t kS8SmemLimit = 232448;  // 227 KB opt-in dynamic shared memory
 
 __host__ __device__ constexpr uint32_t s8_stage_bytes(int bm) {
   return kS8WBytes + static_cast<uint32_t>(bm) * kS8BK + kS8SfBytes;
@@ -100,29 +100,45 @@ __global__ void __launch_bounds__(kS8Threads)
     // ---------------------------------------------------------- producer --
     // While the kernel ahead finishes: the w codes of the ring's first stages into L2.
     for (int it = 0; it < min(total, S); ++it) e_tma_prefetch_2d(&tm_w, (ks0 + it) * kS8BK, n0);
+    const uint8_t* w_sf = p.w_scales + static_cast<size_t>(n0 >> 7) * band_tiles * 512;
+    const uint8_t* x_sf = p.x_scales + static_cast<size_t>(m0 >> 7) * band_tiles * 512;
     griddep_wait();
+    // The loops of both issuing warps carry their slot, phase and addresses
+    // along: with a division by the ring depth and a look at the abort flag a
+    // stage, the instructions of a 16 KB stage took longer than its bytes
+    // (0.38 us a stage on B200, whatever the depth).
     int issued = 0;
-    for (int it = 0; it < total; ++it) {
-      const int s = it % S;
-      if (it >= S && !warp_wait(smem_u32(&empty[s]), ((it / S) - 1) & 1, p.timeout_ns, 80)) {
-        *abort_flag = 1;
+    uint32_t s = 0, ph = 1, fb = smem_u32(full), eb = smem_u32(empty), w_s = sbase;
+    bool ok = true;
+    for (int ks = ks0; ks < ks0 + total; ++ks) {
+      if (issued >= S && !warp_wait(eb, ph, p.timeout_ns, 80)) {
+        ok = false;
         break;
       }
-      if (warp_flag(abort_flag)) break;
-      const uint32_t fb = smem_u32(&full[s]);
-      const uint32_t w_s = sbase + s * stage_bytes;
-      const int ks = ks0 + it;
-      const bool sf = it == 0 || (ks & 3) == 0;  // the scale tiles of a new group of 512 columns
+      const bool sf = issued == 0 || (ks & 3) == 0;  // the scale tiles of a new group of 512 columns
       e_arrive_expect_tx(fb, kS8WBytes + x_bytes + (sf ? kS8SfBytes : 0u));
       e_tma_load_2d(w_s, &tm_w, fb, ks * kS8BK, n0);
       e_tma_load_2d(w_s + kS8WBytes, &tm_x, fb, ks * kS8BK, m0);
       if (sf) {
         const uint32_t sf_s = w_s + kS8WBytes + x_bytes;
-        e_bulk_load(sf_s, p.w_scales + (static_cast<size_t>(n0 >> 7) * band_tiles + (ks >> 2)) * 512, 512u, fb);
-        e_bulk_load(sf_s + 512, p.x_scales + (static_cast<size_t>(m0 >> 7) * band_tiles + (ks >> 2)) * 512, 512u, fb);
+        e_bulk_load(sf_s, w_sf + static_cast<size_t>(ks >> 2) * 512, 512u, fb);
+        e_bulk_load(sf_s + 512, x_sf + static_cast<size_t>(ks >> 2) * 512, 512u, fb);
       }
       ++issued;
+      ++s;
+      fb += 8;
+      eb += 8;
+      w_s += stage_bytes;
+      if (s == static_cast<uint32_t>(S)) {
+        s = 0;
+        ph ^= 1u;
+        fb = smem_u32(full);
+        eb = smem_u32(empty);
+        w_s = sbase;
+        if (warp_flag(abort_flag)) break;
+      }
     }
+    if (!ok) *abort_flag = 1;
     // after an abort: this CTA's own copies land before it may exit
     if (warp_flag(abort_flag))
       for (int c = issued > S ? issued - S : 0; c < issued; ++c)
@@ -133,32 +149,45 @@ __global__ void __launch_bounds__(kS8Threads)
     const uint32_t idesc =
         (1u << 23) | ((static_cast<uint32_t>(p.bm) >> 3) << 17) | (static_cast<uint32_t>(kS8BN >> 4) << 24);
     const uint32_t sf_col = tmem + p.tmem_cols - 32;
-    uint32_t sg = 0;  // scale groups copied
-    for (int it = 0; it < total; ++it) {
-      const int s = it % S;
-      const bool ok = !warp_flag(abort_flag) && warp_wait(smem_u32(&full[s]), (it / S) & 1, p.timeout_ns, 82);
-      if (!ok) {
-        *abort_flag = 1;
-        break;
-      }
+    const uint64_t w_d0 = make_sdesc(sbase, 16, 1024, 2);
+    const uint64_t x_d0 = make_sdesc(sbase + kS8WBytes, 16, 1024, 2);
+    const uint64_t sf_d0 = make_sdesc(sbase + kS8WBytes + x_bytes, 0, 128, 0);
+    const uint32_t step = stage_bytes >> 4;  // descriptor units
+    uint32_t s = 0, ph = 0, fb = smem_u32(full), eb = smem_u32(empty), at = 0;
+    uint32_t sft = sf_col + 16;
+    uint32_t more = 0;  // the first MMA starts the accumulator
+    bool ok = true;
+    for (int ks = ks0; ks < ks0 + total; ++ks) {
+      ok = warp_wait(fb, ph, p.timeout_ns, 82);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t w_s = sbase + s * stage_bytes;
-      const uint32_t x_s = w_s + kS8WBytes;
-      const uint32_t j = static_cast<uint32_t>(ks0 + it) & 3u;
-      if (it == 0 || j == 0) {
-        const uint32_t sft = sf_col + 16 * (sg & 1);
-        e_tmem_cp_32x128b_warpx4(sft, make_sdesc(x_s + x_bytes, 0, 128, 0));
-        e_tmem_cp_32x128b_warpx4(sft + 8, make_sdesc(x_s + x_bytes + 512, 0, 128, 0));
-        ++sg;
+      const uint32_t j = static_cast<uint32_t>(ks) & 3u;
+      if (ks == ks0 || j == 0) {
+        sft ^= (sf_col ^ (sf_col + 16));
+        e_tmem_cp_32x128b_warpx4(sft, sf_d0 + at);
+        e_tmem_cp_32x128b_warpx4(sft + 8, sf_d0 + at + 32);
       }
-      const uint32_t sft = sf_col + 16 * ((sg - 1) & 1);
       const uint32_t id = idesc | (j << 4) | (j << 29);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        e_mma_mxf8(tmem, make_sdesc(w_s + kk * 32, 16, 1024, 2), make_sdesc(x_s + kk * 32, 16, 1024, 2), id, sft,
-                   sft + 8, (it > 0 || kk > 0) ? 1u : 0u);
-      e_commit(smem_u32(&empty[s]));
+      for (int kk = 0; kk < 4; ++kk) {
+        e_mma_mxf8(tmem, w_d0 + at + 2 * kk, x_d0 + at + 2 * kk, id, sft, sft + 8, more);
+        more = 1;
+      }
+      e_commit(eb);
+      ++s;
+      fb += 8;
+      eb += 8;
+      at += step;
+      if (s == static_cast<uint32_t>(S)) {
+        s = 0;
+        ph ^= 1u;
+        fb = smem_u32(full);
+        eb = smem_u32(empty);
+        at = 0;
+        if (warp_flag(abort_flag)) break;
+      }
     }
+    if (!ok) *abort_flag = 1;
     // every MMA (also after an abort) completes before the accumulator is
     // read or the tensor memory released
     e_commit(smem_u32(fin));
@@ -176,12 +205,17 @@ __global__ void __launch_bounds__(kS8Threads)
     const int q = warp & 3;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16);
     float* dst = part + 32 * q + lane;
-    for (int cb = 0; cb < vrows; cb += 16) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(src + cb, v);
+    for (int cb = 0; cb < vrows; cb += 32) {  // bm is a multiple of 16
+      uint32_t v[32];
+      if (cb + 16 < p.bm) tmem_ld_32x32b_x32(src + cb, v);
+      else tmem_ld_32x32b_x16(src + cb, v);
       tmem_ld_wait();
 #pragma unroll
       for (int e = 0; e < 16; ++e) dst[(cb + e) * kS8BN] = __uint_as_float(v[e]);
+      if (cb + 16 < p.bm) {
+#pragma unroll
+        for (int e = 16; e < 32; ++e) dst[(cb + e) * kS8BN] = __uint_as_float(v[e]);
+      }
     }
   }
   if (p.splits > 1) cluster_sync();  // every CTA's partial is in its shared memory
@@ -193,54 +227,41 @@ __global__ void __launch_bounds__(kS8Threads)
 #pragma unroll
     for (int e = 0; e < 4; ++e) b[e] = __bfloat162float(p.bias[n + e]);
   }
-  for (int r = split + p.splits * warp; r < vrows; r += p.splits * (kS8Threads / 32)) {
-    const uint32_t off = part_u + static_cast<uint32_t>((r * kS8BN + 4 * lane) * 4);
-    float4 acc;
-    if (p.splits == 1) {
-      acc = *reinterpret_cast<const float4*>(part + r * kS8BN + 4 * lane);
-    } else {
-      acc = ld_dsmem_f32x4(map_shared_rank(off, 0));
-      for (int src = 1; src < p.splits; ++src) {  // rank order
-        const float4 o = ld_dsmem_f32x4(map_shared_rank(off, static_cast<uint32_t>(src)));
-        acc.x = __fadd_rn(acc.x, o.x);
-        acc.y = __fadd_rn(acc.y, o.y);
-        acc.z = __fadd_rn(acc.z, o.z);
-        acc.w = __fadd_rn(acc.w, o.w);
-      }
-    }
+  // one token of the tile: its 128 channels, four a lane
+  auto store = [&](int r, const float4& acc) {
     float v[4] = {acc.x + b[0], acc.y + b[1], acc.z + b[2], acc.w + b[3]};
     const int64_t m = m0 + r;
     if constexpr (FP8_OUT) {
-      gelu_n<4>(v);
-      if (n >= p.N) v[0] = v[1] = v[2] = v[3] = 0.0f;
-      float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const uint32_t sb = fp8_scale_byte(a);
-      const float inv = fp8_inv_scale(sb);
-      if (!aborted) {
-        if (n < p.N)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.Y) + m * p.N + n) =
-              cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        if (lane == 0) p.y_scales[fp8_scale_offset(m, n0 >> 7, fp8_band_tiles(p.N))] = static_cast<uint8_t>(sb);
-      }
+      if (!aborted) store_gelu_fp8(v, static_cast<uint8_t*>(p.Y), p.y_scales, m, n, p.N, lane);
     } else if (!aborted && n < p.N) {
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.Y) + m * p.N + n) =
           make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
+  };
+  if (p.splits == 1) {
+#pragma unroll 4
+    for (int r = warp; r < vrows; r += kS8Threads / 32)
+      store(r, *reinterpret_cast<const float4*>(part + r * kS8BN + 4 * lane));
+  } else {
+    for (int r = split + p.splits * warp; r < vrows; r += p.splits * (kS8Threads / 32)) {
+      const uint32_t off = part_u + static_cast<uint32_t>((r * kS8BN + 4 * lane) * 4);
+      float4 o[kS8MaxSplits];  // all loads in flight before the first addition
+#pragma unroll
+      for (int src = 0; src < kS8MaxSplits; ++src)
+        o[src] = src < p.splits ? ld_dsmem_f32x4(map_shared_rank(off, static_cast<uint32_t>(src)))
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int src = 1; src < kS8MaxSplits; ++src) {  // rank order; + 0 behind the last rank
+        o[0].x = __fadd_rn(o[0].x, o[src].x);
+        o[0].y = __fadd_rn(o[0].y, o[src].y);
+        o[0].z = __fadd_rn(o[0].z, o[src].z);
+        o[0].w = __fadd_rn(o[0].w, o[src].w);
+      }
+      store(r, o[0]);
+    }
   }
   if constexpr (FP8_OUT) {
-    // zero scales: this tile's block of the band's padding rows, and behind
-    // the row's last block the rest of its word, for every row of the band
-    if (split == 0 && !aborted) {
-      const int64_t y_tiles = fp8_band_tiles(p.N);
-      const int blk = n0 >> 7;
-      for (int r = vrows + tid; r < 128; r += kS8Threads) p.y_scales[fp8_scale_offset(m0 + r, blk, y_tiles)] = 0;
-      if (n0 + kS8BN >= p.N) {
-        for (int z = blk + 1; z < 4 * y_tiles; ++z)
-          for (int r = tid; r < 128; r += kS8Threads) p.y_scales[fp8_scale_offset(m0 + r, z, y_tiles)] = 0;
-      }
-    }
+    if (split == 0 && !aborted) zero_tile_scales(p.y_scales, vrows, m0, n0, p.N, tid, kS8Threads);
   }
   if (p.splits > 1) cluster_sync();  // no CTA leaves while another still reads its partial
   tc_fence_before();

@@ -351,56 +351,127 @@ svdq_status fp8_scales_map(CUtensorMap* map, const void* scales, int64_t rows, i
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Few rows: 128-channel tiles, K split over a cluster.  `bm` tokens a tile
-// (M padded to 16, at most 128).
+// Few rows: 128-channel tiles, K split over a cluster; `bm` tokens a tile (M
+// padded to 16, at most 128).  us: the estimate below, compared with the
+// large-M kernel's.
 struct S8Plan {
   int bm, splits, spc, stages;
   uint32_t tmem_cols;
   size_t smem;
+  double us;
 };
 
-S8Plan s8_plan(int64_t M, int64_t K, int64_t N, int dev, int sms) {
-  S8Plan pl;
-  pl.bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
+// CTAs of the kernel that the device holds at once, as clusters of `splits`.
+int s8_active(const void* kern, int splits, size_t smem, int sms) {
+  if (splits == 1) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, svdq::kS8Threads, smem) != cudaSuccess) return 0;
+    return per_sm * sms;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(splits * sms));
+  cfg.blockDim = dim3(svdq::kS8Threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  return n * splits;
+}
+
+// The split of K and the ring depth with the least estimated time.  The
+// estimate was fitted on B200 to the times of every split from 1 to 8 and
+// depth from 2 to 8 at 50 sizes (M 1 to 256, K 256 to 12288, N 512 to 12288;
+// weights from HBM, launches back to back): with x = bm / 128,
+//   1.0 + 2.4 x  us            launch, start, epilogue
+//   + 2.1 with a cluster, + 0.58 per 100 CTAs (cluster launch and exchange)
+//   + waves spc max(0.32 + 0.016 x, 1.4 / depth)
+//                              a stage: one SM's TMA unit brings 16 KB of
+//                              lines that miss L2 in 0.32 us; below five
+//                              stages a load's latency shows
+//   + 5.4 (waves - 1)          clusters that do not fit at once
+// Its choice costs 2 % over the best one on average, 17 % at the worst.
+svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+  S8Plan best = {};
+  const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
+  const double x = bm / 128.0;
   const int64_t tiles = (N + svdq::kS8BN - 1) / svdq::kS8BN * ((M + svdq::kS8MaxBM - 1) / svdq::kS8MaxBM);
   const int k_stages = static_cast<int>((K + svdq::kS8BK - 1) / svdq::kS8BK);
-  pl.tmem_cols = pow2_at_least(static_cast<uint32_t>(pl.bm + 32));
-  const uint32_t stage = svdq::s8_stage_bytes(pl.bm);
-  const uint32_t fixed = 1024 + svdq::kS8HeadBytes;
-  // ring depth for two CTAs per SM (half of 227 KB less the reserved bytes)
-  const int depth = std::min<int>(svdq::kS8MaxStages, static_cast<int>((115 * 1024 - fixed) / stage));
-  // the split that gives the busiest SM the fewest stages, with two per CTA
-  // for its start and its reduction; the smaller split on ties
-  int best = 1;
-  int64_t best_cost = -1;
+  const uint32_t stage = svdq::s8_stage_bytes(bm);
+  const uint32_t tmem_cols = pow2_at_least(static_cast<uint32_t>(bm + 32));
+  // what a CTA of the deepest ring needs, so that the occupancy calls accept it
+  if (svdq_status rc = ensure_smem(kern, dev, svdq::kS8SmemLimit)) return rc;
   for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
     const int spc = (k_stages + s - 1) / s;
-    if ((k_stages + spc - 1) / spc != s) continue;
-    const int64_t cost = ((tiles * s + sms - 1) / sms) * (spc + 2);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = s;
+    if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
+    for (int depth = std::min(spc, 3); depth <= std::min(spc, 5); ++depth) {
+      const uint32_t ring = std::max<uint32_t>(depth * stage, static_cast<uint32_t>(bm) * svdq::kS8BN * 4);
+      const size_t smem = smem_for_tmem(dev, 1024 + svdq::kS8HeadBytes + ring, tmem_cols);
+      if (smem == 0 || smem > svdq::kS8SmemLimit) continue;
+      const int active = s8_active(kern, s, smem, sms);
+      if (active <= 0) continue;
+      const double ctas = static_cast<double>(tiles) * s;
+      const double waves = std::ceil(ctas / active);
+      const double us = 1.0 + 2.4 * x + (s > 1 ? 2.1 : 0.0) + 0.0058 * ctas +
+                        waves * spc * std::max(0.32 + 0.016 * x, 1.4 / depth) + 5.4 * (waves - 1);
+      if (best.splits == 0 || us < best.us) best = {bm, s, spc, depth, tmem_cols, smem, us};
     }
   }
-  pl.splits = best;
-  pl.spc = (k_stages + best - 1) / best;
-  pl.stages = std::min(pl.spc, depth);
-  uint32_t ring = static_cast<uint32_t>(pl.stages) * stage;
-  ring = std::max<uint32_t>(ring, static_cast<uint32_t>(pl.bm) * svdq::kS8BN * 4);  // the partials
-  pl.smem = smem_for_tmem(dev, fixed + ring, pl.tmem_cols);
-  return pl;
+  if (best.splits == 0) return SVDQ_ERR_CUDA;
+  *out = best;
+  return SVDQ_OK;
+}
+
+// The plan is a pure function of the sizes and the device, so chosen ones are
+// kept (the occupancy calls take tens of microseconds).
+struct S8Key {
+  uint64_t words[4];
+  bool operator==(const S8Key& o) const { return std::memcmp(words, o.words, sizeof(words)) == 0; }
+};
+struct S8KeyHash {
+  size_t operator()(const S8Key& k) const {
+    uint64_t h = 1469598103934665603ull;
+    for (uint64_t w : k.words) h = (h ^ w) * 1099511628211ull;
+    return static_cast<size_t>(h);
+  }
+};
+std::mutex g_s8_mu;
+std::unordered_map<S8Key, S8Plan, S8KeyHash> g_s8_plans;
+
+svdq_status s8_plan_kept(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+  // M only through its tile count and padded tile
+  const uint64_t m_class = M >= svdq::kS8MaxBM ? static_cast<uint64_t>((M + 127) / 128) << 8
+                                               : static_cast<uint64_t>((M + 15) / 16);
+  const S8Key key = {{m_class | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N),
+                      static_cast<uint64_t>(reinterpret_cast<uintptr_t>(kern))}};
+  {
+    std::lock_guard<std::mutex> lock(g_s8_mu);
+    auto it = g_s8_plans.find(key);
+    if (it != g_s8_plans.end()) {
+      *out = it->second;
+      return SVDQ_OK;
+    }
+  }
+  if (svdq_status rc = s8_plan(out, kern, M, K, N, dev, sms)) return rc;
+  std::lock_guard<std::mutex> lock(g_s8_mu);
+  if (g_s8_plans.size() >= kMapCacheCap) g_s8_plans.clear();
+  g_s8_plans.emplace(key, *out);
+  return SVDQ_OK;
 }
 
 template <bool FP8_OUT>
 svdq_status launch_s8(const S8Plan& pl, const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                       const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
-                      uint8_t* y_scales, int dev, void* stream) {
-  if (pl.smem == 0 || pl.smem > 232448) return SVDQ_ERR_CUDA;
+                      uint8_t* y_scales, void* stream) {
   CUtensorMap tm_x, tm_w;
   if (svdq_status rc = fp8_codes_map(&tm_x, x_codes, M, K, static_cast<uint32_t>(pl.bm))) return rc;
   if (svdq_status rc = fp8_codes_map(&tm_w, w_codes, N, K, svdq::kS8BN)) return rc;
   auto kern = svdq::linear_fp8_splitk_kernel<FP8_OUT>;
-  if (svdq_status rc = ensure_smem(reinterpret_cast<const void*>(kern), dev, pl.smem)) return rc;
   svdq::S8Params p;
   p.x_scales = x_scales;
   p.w_scales = w_scales;
@@ -421,6 +492,16 @@ svdq_status launch_s8(const S8Plan& pl, const uint8_t* x_codes, const uint8_t* x
   return launch(kern, grid, svdq::kS8Threads, pl.smem, static_cast<unsigned>(pl.splits), stream, tm_x, tm_w, p);
 }
 
+// The caches of maps and plans allocate: no exception leaves a C call.
+template <typename F>
+svdq_status no_throw(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return SVDQ_ERR_CUDA;
+  }
+}
+
 // The product's entry: Y bf16 [M][N] (y_scales null), or codes [M][N] with
 // y_scales and the GELU epilogue.
 svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
@@ -438,11 +519,22 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (dev < 0) return SVDQ_ERR_CUDA;
   const int sms = sm_count(dev);
   if (sms < 2) return SVDQ_ERR_CUDA;
+  // The few-rows kernel where its estimate is below the large-M kernel's,
+  // 5.2 us + 0.32 us a stage of 128 columns for every wave of CTA pairs
+  // (measured on B200: 13.2 us against 8.2 at 128 x 3072 x 3072, 35.7 against
+  // 18.1 at 256 x 12288 x 3072, but 15.1 against 16.1 at 256 x 3072 x 12288
+  // and 15.5 against 15.9 at 512 x 3072 x 9216).
+  const int64_t pair_tiles = ((M + svdq::kL8BM - 1) / svdq::kL8BM) * ((N + svdq::kL8BN - 1) / svdq::kL8BN);
+  const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
   const int path = g_linear8_path.load(std::memory_order_relaxed);
-  if (path == 2 || (path == 0 && M <= 128)) {
-    const S8Plan pl = s8_plan(M, K, N, dev, sms);
-    return fp8_out ? launch_s8<true>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, dev, stream)
-                   : launch_s8<false>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, dev, stream);
+  if (path == 2 || (path == 0 && M <= 2048)) {
+    const void* kern = fp8_out ? reinterpret_cast<const void*>(svdq::linear_fp8_splitk_kernel<true>)
+                               : reinterpret_cast<const void*>(svdq::linear_fp8_splitk_kernel<false>);
+    S8Plan pl;
+    if (svdq_status rc = s8_plan_kept(&pl, kern, M, K, N, dev, sms)) return rc;
+    if (path == 2 || pl.us < 5.2 + 0.32 * static_cast<double>(pair_waves * ((K + svdq::kL8BK - 1) / svdq::kL8BK)))
+      return fp8_out ? launch_s8<true>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, stream)
+                     : launch_s8<false>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, stream);
   }
 
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y;
@@ -860,13 +952,17 @@ svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int r
 svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                             const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
                             void* stream) {
-  return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, false, stream);
+  return no_throw([&] {
+    return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, false, stream);
+  });
 }
 
 svdq_status svdq_linear_fp8_gelu(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                                  const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N,
                                  uint8_t* y_codes, uint8_t* y_scales, void* stream) {
-  return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, y_codes, y_scales, true, stream);
+  return no_throw([&] {
+    return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, y_codes, y_scales, true, stream);
+  });
 }
 
 svdq_status svdq_attach_lora(const void* L1, const void* L2, const float* lambda, const void* A, const void* B,

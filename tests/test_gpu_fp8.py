@@ -307,7 +307,7 @@ def test_linear_many_tiles(K):
 
 def test_linear_nan_stays_in_its_row(path):
     torch, svdq = _m()
-    for M in (4, 200):
+    for M in (4, 17, 200):
         ten, y, acc = _layer(np.random.default_rng(M), M, 640, 264, False)
         xc = ten[0].view(torch.uint8).clone()
         xc[3, 500] = 0x7F
