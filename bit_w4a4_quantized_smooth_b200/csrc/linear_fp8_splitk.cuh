@@ -47,6 +47,9 @@ struct S8Params {
   uint64_t timeout_ns;
 };
 
+// Never launched: the host asks for this kernel's occupancy.
+__global__ void __launch_bounds__(kS8Threads) linear_fp8_splitk_occupancy_kernel() {}
+
 template <bool FP8_OUT>
 __global__ void __launch_bounds__(kS8Threads)
     linear_fp8_splitk_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,

@@ -361,8 +361,12 @@ struct S8Plan {
   double us;
 };
 
-// CTAs of the kernel that the device holds at once, as clusters of `splits`.
-int s8_active(const void* kern, int splits, size_t smem, int sms) {
+// CTAs of the kernel that the device holds at once, as clusters of `splits`:
+// the occupancy of an empty kernel with the same block and shared memory,
+// because the runtime answers one CTA per SM for any kernel that allocates
+// tensor memory (smem_for_tmem has made shared memory the tighter limit).
+int s8_active(int splits, size_t smem, int sms) {
+  const void* kern = reinterpret_cast<const void*>(svdq::linear_fp8_splitk_occupancy_kernel);
   if (splits == 1) {
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, svdq::kS8Threads, smem) != cudaSuccess) return 0;
@@ -386,16 +390,18 @@ int s8_active(const void* kern, int splits, size_t smem, int sms) {
 
 // The split of K and the ring depth with the least estimated time.  The
 // estimate was fitted on B200 to the times of every split from 1 to 8 and
-// depth from 2 to 8 at 50 sizes (M 1 to 256, K 256 to 12288, N 512 to 12288;
-// weights from HBM, launches back to back): with x = bm / 128,
-//   1.0 + 2.4 x  us            launch, start, epilogue
-//   + 2.1 with a cluster, + 0.58 per 100 CTAs (cluster launch and exchange)
-//   + waves spc max(0.32 + 0.016 x, 1.4 / depth)
-//                              a stage: one SM's TMA unit brings 16 KB of
-//                              lines that miss L2 in 0.32 us; below five
-//                              stages a load's latency shows
-//   + 5.4 (waves - 1)          clusters that do not fit at once
-// Its choice costs 2 % over the best one on average, 17 % at the worst.
+// depth from 2 to 8 at 60 sizes (M 1 to 256, K 256 to 12288, N 512 to 12288;
+// weights from HBM, launches back to back): with x = bm / 128 and `occ` CTAs
+// on an SM,
+//   0.64 + 2.2 x us            launch, start, epilogue
+//   + 1.4 with a cluster, + 0.8 per 100 CTAs (cluster launch and exchange)
+//   + waves spc max(0.37, 1.2 (1 + 0.92 x) / depth, (0.13 + 0.29 x) occ)
+//                              a stage: an SM's TMA unit brings 16 KB of
+//                              lines that miss L2 in about 0.3 us; the latency
+//                              of a load over the ring's depth
+//   + 3.1 (waves - 1)          clusters that do not fit at once
+// Its choice costs 1.3 % over the best one on average, 9.5 % at the worst.
+// The deeper ring on ties.
 svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
@@ -404,21 +410,24 @@ svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t
   const int k_stages = static_cast<int>((K + svdq::kS8BK - 1) / svdq::kS8BK);
   const uint32_t stage = svdq::s8_stage_bytes(bm);
   const uint32_t tmem_cols = pow2_at_least(static_cast<uint32_t>(bm + 32));
-  // what a CTA of the deepest ring needs, so that the occupancy calls accept it
+  const void* model = reinterpret_cast<const void*>(svdq::linear_fp8_splitk_occupancy_kernel);
+  if (svdq_status rc = ensure_smem(model, dev, svdq::kS8SmemLimit)) return rc;
   if (svdq_status rc = ensure_smem(kern, dev, svdq::kS8SmemLimit)) return rc;
   for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
     const int spc = (k_stages + s - 1) / s;
     if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
-    for (int depth = std::min(spc, 3); depth <= std::min(spc, 5); ++depth) {
+    for (int depth = std::min(spc, 3); depth <= std::min(spc, 6); ++depth) {
       const uint32_t ring = std::max<uint32_t>(depth * stage, static_cast<uint32_t>(bm) * svdq::kS8BN * 4);
       const size_t smem = smem_for_tmem(dev, 1024 + svdq::kS8HeadBytes + ring, tmem_cols);
       if (smem == 0 || smem > svdq::kS8SmemLimit) continue;
-      const int active = s8_active(kern, s, smem, sms);
+      const int active = s8_active(s, smem, sms);
       if (active <= 0) continue;
       const double ctas = static_cast<double>(tiles) * s;
       const double waves = std::ceil(ctas / active);
-      const double us = 1.0 + 2.4 * x + (s > 1 ? 2.1 : 0.0) + 0.0058 * ctas +
-                        waves * spc * std::max(0.32 + 0.016 * x, 1.4 / depth) + 5.4 * (waves - 1);
+      const double occ = std::max(1.0, std::min<double>(ctas, active) / sms);
+      const double per = std::max({0.37, 1.2 * (1.0 + 0.92 * x) / depth, (0.13 + 0.29 * x) * occ});
+      const double us = 0.64 + 2.2 * x + (s > 1 ? 1.4 : 0.0) + 0.008 * ctas + waves * spc * per + 3.1 * (waves - 1) -
+                        0.02 * depth;
       if (best.splits == 0 || us < best.us) best = {bm, s, spc, depth, tmem_cols, smem, us};
     }
   }
