@@ -72,6 +72,17 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Results below 2^-126 become 0: three instructions fewer.
+__device__ __forceinline__ float ex2_approx_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -80,27 +91,87 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // ---------------------------------------------------------------- GELU ----
 // GELU(x) = x Phi(x) = max(x, 0) - |x| Phi(-|x|), which has no cancellation
-// for negative x, so the result is good to about 1e-6 relative everywhere
-// (an error against the block's largest value would be too little: small
-// values keep their own E4M3 exponent).
+// for negative x: about 1e-6 relative, also where the result is small (each
+// value keeps its own E4M3 exponent, so an error against the block's largest
+// value would not do).
 //
-// |x| <= 5.5:  Phi(-z) = 2^g(z), g = log2 Phi(-z) as a polynomial of degree
-// 10: one exponential an element and no division (measured on B200: see
-// quantize_fp8_kernel).  The coefficients are this project's own fit: minimax
-// in g (reweighted least squares on Chebyshev nodes, |error| 1.3e-7 in
-// ln Phi), rounded to fp32.
-// |x| > 5.5 (rare; a warp-uniform branch): Phi(-z) = 2^(-z^2 log2(e) / 2) t P(t),
-// t = 1 / (1 + 0.3 z), P of degree 7 fitted to 0.5 erfcx(z / sqrt 2) / t with
-// relative error 1.3e-7 up to z = 13.5, where 2^(...) leaves the fp32 range.
-// The last step rounds toward zero: beyond 5.5 the exact result is below x by
-// less than half an ulp, and rounding up to x itself would turn an E4M3 tie
-// the wrong way.
+// The fast form, |x| <= 5.5: Phi(-z) = 2^g(z) with g = log2 Phi(-z) as a
+// polynomial of degree 10 in -z: one exponential an element, no division (a
+// form with a reciprocal and a degree-7 polynomial needs two of the 16-lane
+// special-function operations an element: 25 us of them alone at 4608 x
+// 12288).  The coefficients are this project's own fit: minimax in g
+// (reweighted least squares on Chebyshev nodes, |error| 1.3e-7 in ln Phi),
+// rounded to fp32.
+// Beyond 5.5 it clamps z: for x > 5.5 that is right to the last bit (the
+// last step rounds toward zero: the exact result lies below x by less than
+// half an ulp, and rounding up to x would turn an E4M3 tie the wrong way); for
+// x < -5.5 it gives -1.05e-7 for a result between that and 0.  In a block
+// whose largest result is 0.1 or more both get the code -0 (half the smallest
+// step is 2^-10 2^-12 = 2.4e-7), so gelu_tail is needed only in a block
+// without any x above 0.3 (GELU(0.3) = 0.185).  Where there is one, it also
+// has the block's largest magnitude: negative results end at -0.17.
 constexpr float kGeluFast = 5.5f;
+constexpr float kGeluPos = 0.3f, kGeluPosResult = 0.18f;  // GELU(0.3) = 0.1854
 
+__device__ __forceinline__ uint64_t fma_rz_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// n values (n even), coefficient by coefficient: the n / 2 chains of packed
+// operations are independent, and a coefficient's register pair is set once
+// for all of them.
+template <int n>
+__device__ __forceinline__ void gelu_fast(float* x) {
+  constexpr float c[11] = {-0.9999998211860657f,    1.1511125564575195f,    -0.4591609537601471f,
+                           0.05260409042239189f,    0.007166661322116852f,  0.00016647009761072695f,
+                           -0.0002045672881649807f, -5.589646752923727e-05f, -7.6225755947234575e-06f,
+                           -5.619402827505837e-07f, -1.7772931570902983e-08f};
+  uint64_t nz[n / 2], g[n / 2];
+#pragma unroll
+  for (int i = 0; i < n / 2; ++i)
+    nz[i] = pack_f32x2(max_nan(-fabsf(x[2 * i]), -kGeluFast), max_nan(-fabsf(x[2 * i + 1]), -kGeluFast));
+  {
+    const uint64_t a = pack_f32x2(c[10], c[10]), b = pack_f32x2(c[9], c[9]);
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) g[i] = fma_f32x2(a, nz[i], b);
+  }
+#pragma unroll
+  for (int k = 8; k >= 0; --k) {
+    const uint64_t b = pack_f32x2(c[k], c[k]);
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) g[i] = fma_f32x2(g[i], nz[i], b);
+  }
+#pragma unroll
+  for (int i = 0; i < n / 2; ++i) {
+    float g0, g1;
+    unpack_f32x2(g[i], g0, g1);
+    unpack_f32x2(fma_rz_f32x2(nz[i], pack_f32x2(ex2_approx_ftz(g0), ex2_approx_ftz(g1)),
+                              pack_f32x2(fmaxf(x[2 * i], 0.0f), fmaxf(x[2 * i + 1], 0.0f))),
+                 x[2 * i], x[2 * i + 1]);
+  }
+}
+
+// x < -5.5: Phi(-z) = 2^(-z^2 log2(e) / 2) t P(t), t = 1 / (1 + 0.3 z), P of
+// degree 7 fitted the same way to 0.5 erfcx(z / sqrt 2) / t with relative
+// error 1.3e-7 up to z = 13.5; beyond, the result leaves fp32's normal range.
+// The exponent reaches 131, where one rounding is worth 2.6e-6 of the result,
+// so it is carried as a sum of two parts.
 __device__ __forceinline__ float gelu_tail(float x) {
-  const float z = fabsf(x);
-  const float zc = fminf(z, 13.5f);
-  const float t = rcp_approx(__fmaf_rn(zc, 0.3f, 1.0f));
+  constexpr float c_hi = 0.72134751081466675f, c_lo = 9.6298140e-9f;  // log2(e) / 2
+  const float z = fminf(-x, 30.0f);
+  const float sq = __fmul_rn(z, z);
+  const float e = __fmul_rn(sq, c_hi);
+  const float lo = __fmaf_rn(sq, c_hi, -e) + __fmaf_rn(__fmaf_rn(z, z, -sq), c_hi, sq * c_lo);
+  const float t = rcp_approx(__fmaf_rn(z, 0.3f, 1.0f));
   float q = 0.03593172878026962f;
   q = __fmaf_rn(q, t, -0.15827596187591553f);
   q = __fmaf_rn(q, t, 0.20820654928684235f);
@@ -109,50 +180,55 @@ __device__ __forceinline__ float gelu_tail(float x) {
   q = __fmaf_rn(q, t, 0.09963750094175339f);
   q = __fmaf_rn(q, t, 0.12079835683107376f);
   q = __fmaf_rn(q, t, 0.11962638795375824f);
-  q = __fmul_rn(__fmul_rn(q, t), ex2_approx(__fmul_rn(__fmul_rn(zc, zc), -0.72134752044448170f)));
-  return __fmaf_rz(-z, q, fmaxf(x, 0.0f));
+  q = __fmul_rn(q, __fmaf_rn(t, -0.69314718f * lo, t));  // 2^-lo to first order
+  return __fmul_rz(-z, __fmul_rn(q, ex2_approx(-e)));
 }
 
-__device__ __forceinline__ void gelu2_fast(float& x0, float& x1) {
-  const float z0 = fabsf(x0), z1 = fabsf(x1);
-  const uint64_t z = pack_f32x2(fminf(z0, kGeluFast), fminf(z1, kGeluFast));
-  constexpr float c[11] = {-0.9999998211860657f,     -1.1511125564575195f,    -0.4591609537601471f,
-                           -0.05260409042239189f,    0.007166661322116852f,   -0.00016647009761072695f,
-                           -0.0002045672881649807f,  5.589646752923727e-05f,  -7.6225755947234575e-06f,
-                           5.619402827505837e-07f,   -1.7772931570902983e-08f};
-  uint64_t g = pack_f32x2(c[10], c[10]);
-#pragma unroll
-  for (int i = 9; i >= 0; --i) g = fma_f32x2(g, z, pack_f32x2(c[i], c[i]));
-  float g0, g1;
-  unpack_f32x2(g, g0, g1);
-  x0 = __fmaf_rz(-z0, ex2_approx(g0), fmaxf(x0, 0.0f));
-  x1 = __fmaf_rz(-z1, ex2_approx(g1), fmaxf(x1, 0.0f));
-}
-
-// GELU of n values in registers (n even); all lanes of the warp call it.
 template <int n>
-__device__ __forceinline__ void gelu_n(float* v) {
-  float top = 0.0f;
+__device__ __forceinline__ float amax_n(const float* v) {
+  float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < n; ++i) top = fmaxf(top, fabsf(v[i]));
-  if (__any_sync(0xffffffffu, top > kGeluFast)) {
+  for (int i = 0; i < n; ++i) a = fmaxf(a, fabsf(v[i]));
+  return a;
+}
+
+// The largest of n values (n even), NaN ignored.
+template <int n>
+__device__ __forceinline__ float max_n(const float* v) {
+  float a = fmaxf(v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < n; i += 2) {
-      float a = v[i], b = v[i + 1];
-      gelu2_fast(a, b);
-      v[i] = fabsf(v[i]) > kGeluFast ? gelu_tail(v[i]) : a;
-      v[i + 1] = fabsf(v[i + 1]) > kGeluFast ? gelu_tail(v[i + 1]) : b;
+  for (int i = 2; i < n; i += 2) a = max3(a, v[i], v[i + 1]);
+  return a;
+}
+
+// GELU of this lane's n values (n even) of a block spread over `lanes`
+// neighbouring lanes, and the block's largest magnitude.  All lanes call it.
+template <int n, int lanes>
+__device__ __forceinline__ float gelu_block(float* v) {
+  float x[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) x[i] = v[i];
+  gelu_fast<n>(v);
+  float a = max_n<n>(v);
+#pragma unroll
+  for (int o = lanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  const bool careful = !(a > kGeluPosResult);
+  if (__any_sync(0xffffffffu, careful)) {
+    if (careful) {
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (x[i] < -kGeluFast) v[i] = gelu_tail(x[i]);
     }
-  } else {
+    a = amax_n<n>(v);
 #pragma unroll
-    for (int i = 0; i < n; i += 2) gelu2_fast(v[i], v[i + 1]);
+    for (int o = lanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   }
+  return a;
 }
 
 // ------------------------------------------------------------- elements ----
 // Eight consecutive elements of a row.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
   v[0] = bf16_lo(w.x);
   v[1] = bf16_hi(w.x);
   v[2] = bf16_lo(w.y);
@@ -161,6 +237,9 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
   v[5] = bf16_hi(w.z);
   v[6] = bf16_lo(w.w);
   v[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
 }
 __device__ __forceinline__ void load8(const float* p, float* v) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -181,13 +260,18 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ float amax8(const float* v) {
-  return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-               fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+__device__ __forceinline__ float amax8(const float* v) { return amax_n<8>(v); }
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
+  float a, b, c, d;
+  mul2_rn(a, b, v[0], v[1], inv, inv);
+  mul2_rn(c, d, v[2], v[3], inv, inv);
+  return cvt_e4m3x4(a, b, c, d);
 }
 __device__ __forceinline__ uint2 codes8(const float* v, float inv) {
-  return make_uint2(cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                    cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+  return make_uint2(codes4(v, inv), codes4(v + 4, inv));
+}
+__device__ __forceinline__ uint4 codes16(const float* v, float inv) {
+  return make_uint4(codes4(v, inv), codes4(v + 4, inv), codes4(v + 8, inv), codes4(v + 12, inv));
 }
 // Maximum over the 16 lanes that hold one block (8 elements each).
 __device__ __forceinline__ float block_max16(float a) {
@@ -210,15 +294,12 @@ __device__ __forceinline__ void zero_pad_scales(uint8_t* scales, int64_t M, int6
 // written.
 __device__ __forceinline__ void store_gelu_fp8(float* v, uint8_t* codes, uint8_t* scales, int64_t m, int n, int N,
                                                int lane) {
-  gelu_n<4>(v);
-  if (n >= N) v[0] = v[1] = v[2] = v[3] = 0.0f;
-  float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if (n >= N) v[0] = v[1] = v[2] = v[3] = 0.0f;  // GELU(0) = 0
+  const float a = gelu_block<4, 32>(v);
   const uint32_t b = fp8_scale_byte(a);
   const float inv = fp8_inv_scale(b);
   if (n < N)
-    *reinterpret_cast<uint32_t*>(codes + m * N + n) = cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    *reinterpret_cast<uint32_t*>(codes + m * N + n) = codes4(v, inv);
   if (lane == 0) scales[fp8_scale_offset(m, n >> 7, fp8_band_tiles(N))] = static_cast<uint8_t>(b);
 }
 
@@ -237,46 +318,68 @@ __device__ __forceinline__ void zero_tile_scales(uint8_t* scales, int rows, int6
 
 // ============================================================ quantiser ====
 // x codes and scales of X (or GELU(X)), bf16 [M][K] with row stride ldx.
-// Thread = 8 columns of kQ8Rows consecutive rows (one 16-byte load each, all
-// in flight together), 16 lanes = one block.  HBM-bound: 2 + 1 bytes an
-// element.  The grid's last x index zeroes the padding rows' scales.
-constexpr int kQ8Threads = 256;
-constexpr int kQ8Rows = 4;
+// HBM-bound: 2 + 1 bytes an element.  A warp takes 512 columns (one scale
+// tile's four blocks) of R consecutive rows: a lane holds 16 columns of each
+// row (two 16-byte loads a row, all R rows' in flight before the first is
+// used: 128 bytes a thread at R = 4), 8 lanes a block; a row's four scale
+// bytes leave as one word.  (A first version with 8 columns a lane, 4 rows and
+// single scale bytes took 43.1 us for 4608 x 12288 of 21504 columns on B200,
+// 59.4 with GELU: half the loads in flight, and 2.7 us for the byte stores.)
+// The grid's last block zeroes the padding rows' scales.
+constexpr int kQ8Threads = 128;
 
-template <bool GELU>
+template <int R, bool GELU>
 __global__ void __launch_bounds__(kQ8Threads)
     quantize_fp8_kernel(const __nv_bfloat16* __restrict__ X, int64_t ldx, int M, int K, uint8_t* __restrict__ codes,
                         uint8_t* __restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t band_tiles = fp8_band_tiles(K);
+  const int band_tiles = static_cast<int>(fp8_band_tiles(K));
   if (blockIdx.x == gridDim.x - 1) {
-    if (blockIdx.y == 0) zero_pad_scales(scales, M, band_tiles, threadIdx.x, kQ8Threads);
+    zero_pad_scales(scales, M, band_tiles, threadIdx.x, kQ8Threads);
     return;
   }
-  const int c8 = blockIdx.y * kQ8Threads + threadIdx.x;  // 8-column chunk
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kQ8Rows;
-  const int blk = c8 >> 4;
-  if (blk >= 4 * band_tiles) return;                     // whole 16-lane groups, and whole warps unless K ends in one
-  const bool in = 8 * c8 < K;
-  float v[kQ8Rows][8];
+  const int lane = threadIdx.x & 31;
+  const int w = blockIdx.x * (kQ8Threads / 32) + (threadIdx.x >> 5);  // 512-column segment, fastest along the row
+  const int seg = w % band_tiles;
+  const int row0 = (w / band_tiles) * R;
+  if (row0 >= M) return;  // whole warps
+  const int col = 512 * seg + 16 * lane;
+  const bool in = col < K;  // K is a multiple of 16
+  uint4 raw[R][2];
 #pragma unroll
-  for (int i = 0; i < kQ8Rows; ++i) {
+  for (int i = 0; i < R; ++i) {
+    raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
     if (in && row0 + i < M) {
-      load8(X + (row0 + i) * ldx + 8 * c8, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      const uint4* src = reinterpret_cast<const uint4*>(X + (row0 + i) * ldx + col);
+      raw[i][0] = __ldcs(src);
+      raw[i][1] = __ldcs(src + 1);
     }
   }
+  uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < kQ8Rows; ++i) {
-    if (row0 + i >= M) break;
-    if constexpr (GELU) gelu_n<8>(v[i]);
-    const uint32_t b = fp8_scale_byte(block_max16(amax8(v[i])));
-    if (in) *reinterpret_cast<uint2*>(codes + (row0 + i) * K + 8 * c8) = codes8(v[i], fp8_inv_scale(b));
-    if ((c8 & 15) == 0) scales[fp8_scale_offset(row0 + i, blk, band_tiles)] = static_cast<uint8_t>(b);
+  for (int i = 0; i < R; ++i) {
+    float v[16];
+    unpack8(raw[i][0], v);
+    unpack8(raw[i][1], v + 8);
+    float a;
+    if constexpr (GELU) {
+      a = gelu_block<16, 8>(v);
+    } else {
+      a = amax_n<16>(v);
+#pragma unroll
+      for (int o = 4; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    }
+    const uint32_t b = fp8_scale_byte(a);
+    if (in && row0 + i < M)
+      *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row0 + i) * K + col) = codes16(v, fp8_inv_scale(b));
+    uint32_t t = b << (lane & 24);  // the row's four bytes, in every lane
+    t |= __shfl_xor_sync(0xffffffffu, t, 8);
+    t |= __shfl_xor_sync(0xffffffffu, t, 16);
+    if (lane == i) word = t;
   }
+  if (lane < R && row0 + lane < M)
+    *reinterpret_cast<uint32_t*>(scales + fp8_scale_offset(row0 + lane, 4 * seg, band_tiles)) = word;
 }
 
 // ============================================================ RMS norm ====
@@ -422,11 +525,7 @@ __global__ void __launch_bounds__(kPw8Threads)
       const int k = k0 + 32 * part + 16 * j;
       const float* s = v + 16 * j;
       if (k < K)
-        *reinterpret_cast<uint4*>(codes + row * K + k) = make_uint4(
-            cvt_e4m3x4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv),
-            cvt_e4m3x4(s[4] * inv, s[5] * inv, s[6] * inv, s[7] * inv),
-            cvt_e4m3x4(s[8] * inv, s[9] * inv, s[10] * inv, s[11] * inv),
-            cvt_e4m3x4(s[12] * inv, s[13] * inv, s[14] * inv, s[15] * inv));
+        *reinterpret_cast<uint4*>(codes + row * K + k) = codes16(s, inv);
     }
   }
   // rows past N are zeros in the tile: their scale byte is 0

@@ -11,8 +11,8 @@
 namespace svdq {
 
 // Persistent CTA pairs (clusters of 2): grid = 2 x min(pair tiles, SMs / 2),
-// 192 threads per CTA: warp 0 TMA producer, warp 1 TMEM owner and (even CTA)
-// MMA issuer, warps 2-5 epilogue; the roles, the hand-offs and the abort
+// 192 threads per CTA (320 with the FP8 output): warp 0 TMA producer, warp 1
+// TMEM owner and (even CTA) MMA issuer, the others epilogue; the roles, the hand-offs and the abort
 // drain are those of the 4-bit kernel (linear.cuh).
 // A pair computes 256 x 256 output tiles, visited M-fastest; CTA c holds 128
 // of the tile's x rows and 128 of its w rows, the even CTA issues 2-SM MMAs
@@ -28,7 +28,7 @@ namespace svdq {
 // in order, so the regions alternate without a barrier.
 // Accumulators: two 128 x 256 fp32 tiles overlap in each CTA's TMEM as in the
 // 4-bit kernel: columns [0, 256) and [192, 448), scales in [448, 480).
-constexpr int kL8Threads = 192;
+constexpr int kL8Threads = 192, kL8ThreadsFp8 = 320;
 constexpr int kL8Stages = 6;
 constexpr int kL8BM = 256, kL8BN = 256, kL8BK = 128;
 constexpr uint32_t kL8ABytes = 16384, kL8BBytes = 16384;
@@ -46,16 +46,22 @@ constexpr uint32_t kL8SfCol = 448;                    // region p: x scales at +
 
 struct L8Params {
   const __nv_bfloat16* bias;
-  uint8_t* y_scales;   // FP8 output: scale tiles of the output rows
+  uint8_t* y_codes;    // FP8 output [M][N], and its scale tiles
+  uint8_t* y_scales;
   int M, K, N;
   int m_tiles, tiles;  // pair tiles: ceil(M / 256) x ceil(N / 256)
   uint64_t timeout_ns;
 };
 
-// FP8_OUT: GELU and FP8 block-128 output (two blocks per tile row, each wholly
-// in one epilogue thread); otherwise bf16.
+// FP8_OUT: GELU and FP8 block-128 output.  Two warpgroups of epilogue warps
+// take one 128-column block of the tile each; a thread holds one row's whole
+// block, so the block's scale needs no exchange, and the row's 128 code bytes
+// leave as eight 16-byte stores.  (With four warps for both blocks the
+// epilogue took longer than the MMAs of a 3072-wide tile: 172 us against 153
+// without GELU at 4608 x 3072 x 12288, sustained.)  Otherwise bf16 through a
+// staging block and TMA stores.
 template <bool FP8_OUT>
-__global__ void __launch_bounds__(kL8Threads, 1)
+__global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws,
                       const __grid_constant__ CUtensorMap tm_y, const L8Params p) {
@@ -66,7 +72,7 @@ __global__ void __launch_bounds__(kL8Threads, 1)
   uint64_t* full = bars;                          // [S] even CTA: both CTAs' stage landed
   uint64_t* empty = full + kL8Stages;             // [S] the stage's MMAs and copies are done
   uint64_t* acc_full = empty + kL8Stages;         // [2] tile accumulated (both CTAs)
-  uint64_t* acc_empty = acc_full + 2;             // [2] even CTA: 8 epilogue warps drained it
+  uint64_t* acc_empty = acc_full + 2;             // [2] even CTA: both CTAs' epilogue warps drained it
   uint64_t* ovl_free = acc_empty + 2;             // even CTA: shared columns drained
   uint64_t* fin = ovl_free + 1;                   // even CTA: every MMA complete
   uint64_t* odd_done = fin + 1;                   // even CTA: the odd producer published its count
@@ -95,7 +101,7 @@ __global__ void __launch_bounds__(kL8Threads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 8);
+      mbar_init(smem_u32(&acc_empty[b]), FP8_OUT ? 16 : 8);
     }
     mbar_init(smem_u32(ovl_free), 8);
     mbar_init(smem_u32(fin), 1);
@@ -228,23 +234,24 @@ __global__ void __launch_bounds__(kL8Threads, 1)
   } else {
     // ------------------------------------------------------- epilogue --
     griddep_wait();            // the bias and Y may belong to the kernel ahead
-    const int et = tid - 64;   // 0..127
+    const int wg = FP8_OUT ? (warp - 2) >> 2 : 0;  // FP8 output: the warpgroup's block of the tile
+    const int et = (tid - 64) & 127;
     const int q = warp & 3;    // TMEM lane quadrant this warp may access
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    uint8_t* blk = smem + kL8OutOffset + (warp - 2) * kL8OutBytes;
+    uint8_t* blk = smem + kL8OutOffset + ((warp - 2) & 3) * kL8OutBytes;  // bf16 output only
     uint8_t* rowp = blk + lane * 128;
     int i = 0;
     for (int t = pair; t < p.tiles; t += pairs, ++i) {
       const int b = i & 1;
       const int m0 = ((t % p.m_tiles) * 2 + static_cast<int>(rank)) * 128;
       const int n0 = (t / p.m_tiles) * kL8BN;
-      named_bar_sync(1, 128);  // everyone is done with the previous tile's bias
-      for (int j = et; j < kL8BN; j += 128) {
+      named_bar_sync(1 + wg, 128);  // everyone is done with the previous tile's bias
+      for (int j = FP8_OUT ? 128 * wg + et : et; j < (FP8_OUT ? 128 * wg + 128 : kL8BN); j += 128) {
         const int n = n0 + j;
         bias_s[j] = (p.bias && n < N) ? __bfloat162float(p.bias[n]) : 0.0f;
       }
-      named_bar_sync(1, 128);
-      // no early exit: all four warps must keep meeting the named barriers
+      named_bar_sync(1 + wg, 128);
+      // no early exit: the warps of a group must keep meeting its named barrier
       const bool ok = !warp_flag(abort_flag) && warp_wait(smem_u32(&acc_full[b]), (i >> 1) & 1, p.timeout_ns, 70);
       if (!ok) {
         *abort_flag = 1;
@@ -253,65 +260,76 @@ __global__ void __launch_bounds__(kL8Threads, 1)
       tc_fence_after();
       const uint32_t acc_col = b ? kL8Acc1Col : 0u;
       if constexpr (FP8_OUT) {
-        uint32_t sbytes = 0;
-#pragma unroll 1
-        for (int gi = 0; gi < 2; ++gi) {
-          // the 128-column block that holds the 64 shared columns first
-          const int h = b ? gi : 1 - gi;
-          float v[128];
+        const uint32_t src = tmem + lane_base + acc_col + 128 * wg;
+        float v[128];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 128 * h + 32 * j, reinterpret_cast<uint32_t*>(v) + 32 * j);
-          tmem_ld_wait();
+        for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(src + 32 * j, reinterpret_cast<uint32_t*>(v) + 32 * j);
+        tmem_ld_wait();
+        const float* bs = bias_s + 128 * wg;
+        const int nb = n0 + 128 * wg;
+        const int valid = N - nb;  // columns of the block below N; the others have zero weights and bias, GELU(0) = 0
+#pragma unroll
+        for (int j = 0; j < 128; j += 2) {
+          float2 c = *reinterpret_cast<const float2*>(bs + j);
+          add2_rn(v[j], v[j + 1], v[j], v[j + 1], c.x, c.y);
+        }
+        // a row without an x above 0.3 needs more care (fp8.cuh): then its
+        // accumulators are read again, 16 columns at a time, before they are
+        // released
+        const float hi = max_n<128>(v);
+        const bool careful = !(hi > kGeluPos);
+        const bool any_careful = __any_sync(0xffffffffu, careful);
+        if (!any_careful) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(lead(gi == 0 ? ovl_free : &acc_empty[b]));
-          const float* bs = bias_s + 128 * h;
-          const int valid = N - (n0 + 128 * h);  // columns of the block below N
-          float a = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 128; j += 16) {
-#pragma unroll
-            for (int e = j; e < j + 16; ++e) v[e] += bs[e];
-            gelu_n<16>(v + j);
-            if (valid < 128) {
-#pragma unroll
-              for (int e = j; e < j + 16; ++e) v[e] = e < valid ? v[e] : 0.0f;
-            }
-#pragma unroll
-            for (int e = j; e < j + 16; ++e) a = fmaxf(a, fabsf(v[e]));
-          }
-          const uint32_t sb = fp8_scale_byte(a);
-          sbytes |= sb << (8 * h);
-          const float inv = fp8_inv_scale(sb);
-          if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {  // 16-byte chunk j = columns 16 j .. 16 j + 15
-            const float* c = v + 16 * j;
-            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(cvt_e4m3x4(c[0] * inv, c[1] * inv, c[2] * inv, c[3] * inv),
-                           cvt_e4m3x4(c[4] * inv, c[5] * inv, c[6] * inv, c[7] * inv),
-                           cvt_e4m3x4(c[8] * inv, c[9] * inv, c[10] * inv, c[11] * inv),
-                           cvt_e4m3x4(c[12] * inv, c[13] * inv, c[14] * inv, c[15] * inv));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && valid > 0 && m0 + 32 * q < p.M) {
-            tma_store_2d(&tm_y, smem_u32(blk), n0 + 128 * h, m0 + 32 * q);
-            bulk_commit_group();
+          if (lane == 0) {
+            if (wg != b) mbar_arrive_remote(lead(ovl_free));  // this block holds the 64 shared columns
+            mbar_arrive_remote(lead(&acc_empty[b]));
           }
         }
-        // the row's two scale bytes: half of a word of four blocks; the last
-        // tile of an odd number writes the word's other half as zeros too.
-        // Padding rows of the last 128-row band get zeros.
+#pragma unroll
+        for (int j = 0; j < 128; j += 16) gelu_fast<16>(v + j);
+        float top[2] = {hi, 0.0f};
+        gelu_fast<2>(top);
+        float amax = top[0];
+        if (any_careful) {
+#pragma unroll
+          for (int j = 0; j < 128; j += 16) {
+            uint32_t w[16];
+            tmem_ld_32x32b_x16(src + j, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = __uint_as_float(w[e]) + bs[j + e];
+              if (careful && x < -kGeluFast) v[j + e] = gelu_tail(x);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (wg != b) mbar_arrive_remote(lead(ovl_free));
+            mbar_arrive_remote(lead(&acc_empty[b]));
+          }
+          if (careful) amax = amax_n<128>(v);
+        }
+        const uint32_t sb = fp8_scale_byte(amax);
+        const float inv = fp8_inv_scale(sb);
         const int m = m0 + 32 * q + lane;
+        if (m < p.M) {
+          uint8_t* dst = p.y_codes + static_cast<int64_t>(m) * N + nb;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {  // N is a multiple of 16
+            if (16 * j < valid)
+              *reinterpret_cast<uint4*>(dst + 16 * j) = codes16(v + 16 * j, inv);
+          }
+        }
+        // the block's scale byte; the last tile's second block also writes the
+        // rest of the row's last word.  Padding rows of the last 128-row band
+        // get zeros.
         if (m0 < p.M) {
-          if (m >= p.M) sbytes = 0;
-          const int64_t y_tiles = fp8_band_tiles(N);
-          uint8_t* dst = p.y_scales + fp8_scale_offset(m, n0 >> 7, y_tiles);
-          if (((n0 >> 8) & 1) == 0 && n0 + kL8BN >= N) *reinterpret_cast<uint32_t*>(dst) = sbytes;
-          else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sbytes);
+          uint8_t* dst = p.y_scales + fp8_scale_offset(m, nb >> 7, fp8_band_tiles(N));
+          *dst = m < p.M ? static_cast<uint8_t>(sb) : uint8_t{0};
+          if (wg == 1 && ((n0 >> 8) & 1) == 0 && n0 + kL8BN >= N) *reinterpret_cast<uint16_t*>(dst + 1) = 0;
         }
       } else {
 #pragma unroll 1

@@ -552,7 +552,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (svdq_status rc = fp8_scales_map(&tm_xs, x_scales, M, K)) return rc;
   if (svdq_status rc = fp8_scales_map(&tm_ws, w_scales, N, K)) return rc;
   if (fp8_out) {
-    if (svdq_status rc = fp8_codes_map(&tm_y, Y, M, N, 32)) return rc;  // one epilogue warp's 32 x 128 block
+    std::memset(&tm_y, 0, sizeof(tm_y));  // codes are stored from registers
   } else {
     const uint64_t dims[2] = {static_cast<uint64_t>(N), static_cast<uint64_t>(M)};
     const uint64_t strides[1] = {static_cast<uint64_t>(N) * 2};
@@ -563,6 +563,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   }
   svdq::L8Params p;
   p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.y_codes = fp8_out ? static_cast<uint8_t*>(Y) : nullptr;
   p.y_scales = y_scales;
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
@@ -574,7 +575,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   auto kern = fp8_out ? svdq::linear_fp8_kernel<true> : svdq::linear_fp8_kernel<false>;
   if (svdq_status rc = ensure_smem(reinterpret_cast<const void*>(kern), dev, smem)) return rc;
   const int pairs = p.tiles < sms / 2 ? p.tiles : sms / 2;
-  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), svdq::kL8Threads, smem, 2, stream, tm_x, tm_w, tm_xs,
+  return launch(kern, dim3(static_cast<unsigned>(2 * pairs)), fp8_out ? svdq::kL8ThreadsFp8 : svdq::kL8Threads, smem, 2, stream, tm_x, tm_w, tm_xs,
                 tm_ws, tm_y, p);
 }
 
@@ -934,11 +935,19 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
     return SVDQ_ERR_INVALID_ARG;
   if (K % 16 != 0 || ldx % 8 != 0 || M > kMaxRows || K > kMaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(X) || !aligned16(x_codes) || !aligned16(x_scales)) return SVDQ_ERR_MISALIGNED;
-  const dim3 grid(static_cast<unsigned>((M + svdq::kQ8Rows - 1) / svdq::kQ8Rows + 1),
-                  static_cast<unsigned>((64 * svdq::fp8_band_tiles(K) + svdq::kQ8Threads - 1) / svdq::kQ8Threads));
-  return launch(gelu ? svdq::quantize_fp8_kernel<true> : svdq::quantize_fp8_kernel<false>, grid, svdq::kQ8Threads, 0, 1,
-                stream, static_cast<const __nv_bfloat16*>(X), ldx, static_cast<int>(M), static_cast<int>(K), x_codes,
-                x_scales);
+  // rows a warp: one while that gives fewer than 64 warps an SM, else 4
+  const int dev = current_device();
+  if (dev < 0) return SVDQ_ERR_CUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return SVDQ_ERR_CUDA;
+  const int64_t segs = svdq::fp8_band_tiles(K);
+  const int rows = M * segs <= 64 * static_cast<int64_t>(sms) ? 1 : 4;
+  const int64_t warps = (M + rows - 1) / rows * segs;
+  const dim3 grid(static_cast<unsigned>((warps + svdq::kQ8Threads / 32 - 1) / (svdq::kQ8Threads / 32) + 1));
+  auto kern = rows == 1 ? (gelu ? svdq::quantize_fp8_kernel<1, true> : svdq::quantize_fp8_kernel<1, false>)
+                        : (gelu ? svdq::quantize_fp8_kernel<4, true> : svdq::quantize_fp8_kernel<4, false>);
+  return launch(kern, grid, svdq::kQ8Threads, 0, 1, stream, static_cast<const __nv_bfloat16*>(X), ldx,
+                static_cast<int>(M), static_cast<int>(K), x_codes, x_scales);
 }
 
 svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int residual_dtype, const void* gamma,

@@ -272,7 +272,6 @@ svdq_status svdq_pack_weight_fp8(const void* W, int w_dtype, int64_t K, int64_t 
  *             about 1e-6 relative also for negative x, not rounded to bf16
  *             before the quantiser.  (svdq_quantize_act_gelu evaluates the
  *             same function by an approximation with 3e-7 absolute error.)
- *             An infinite x gives NaN.
  *   x_codes   uint8 [M][K] output;   x_scales   svdq_fp8_sizes(M, K) output
  */
 svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, int gelu, uint8_t* x_codes,

@@ -5,6 +5,8 @@ Tolerances, from the arithmetic of each call (u = 2^-24, half an fp32 step):
 - GELU: |error| <= 2^-19 |GELU(x)| for inputs in [-13, 13]: the fit of
   log2 Phi is within 1.3e-7 in ln Phi, its fp32 evaluation (|g| <= 27, ten
   fused steps) adds up to about 8e-7, the exponential 2 u, the last product u.
+  (In a block whose largest result is 0.1 or more, values of x < -5.5 are
+  -1.05e-7 or nearer to 0 on both sides, below half the smallest code.)
 - norm: the sum of squares is a chain of at most 32 fused steps, then two
   five-step trees, so 42 u relative, of which the root takes half; division,
   addition, root, two products: 5 u more.  26 u < 2^-19.
@@ -133,6 +135,42 @@ def test_gelu_over_its_range():
     _ok()
     g = ref.gelu(_np(X))
     ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
+
+
+@pytest.mark.parametrize("path", ["large", "small"])
+def test_fused_gelu_of_deep_negative_rows(path):
+    """Rows whose results are all tiny, all in the far tail, or mixed: the
+    product passes x through (w the identity), so the GELU's tail is reached."""
+    torch, svdq = _m()
+    K = 256
+    rng = np.random.default_rng(5)
+    x = np.stack([np.linspace(-13, -6, K), np.linspace(-9, 0.1, K), np.linspace(-30, 3, K), np.linspace(-5.6, -5.4, K),
+                  rng.normal(size=K) * 3 - 6, np.linspace(-12, 0.19, K), np.linspace(-12, 0.21, K), np.zeros(K)])
+    (xc, xs), (wc, ws) = ref.encode(np.repeat(x, 40, axis=0)), ref.encode(np.eye(K))
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    t = lambda a, d: torch.from_numpy(a).cuda().view(d)
+    svdq.set_linear_fp8_path(path)
+    try:
+        codes, scales = svdq.linear_fp8_gelu(t(xc, f8), t(ref.tiles(xs), e8), t(wc, f8), t(ref.tiles(ws), e8))
+    finally:
+        svdq.set_linear_fp8_path("auto")
+    _ok()
+    g = ref.gelu(ref.decode(xc, xs))                       # the product itself is exact
+    ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
+
+
+def test_gelu_of_nan_and_infinity():
+    torch, svdq = _m()
+    Y = torch.ones((3, 256), dtype=torch.bfloat16, device="cuda")
+    Y[0, 5], Y[1, 7], Y[2, 200] = float("nan"), float("inf"), float("-inf")
+    Y[2, 201:] = -9.0
+    codes, scales = svdq.quantize_fp8(Y, gelu=True)
+    _ok()
+    v = codes.float().cpu()
+    s, _ = ref.untile(_np(scales), 3, 256)
+    assert torch.isnan(v[0, 5]) and torch.isnan(v).sum() == 1 and (v[0, 6:] == v[0, 6]).all()
+    assert s[1, 0] == 247 and v[1, 7] == 448 and (v[1, :7] == 0).all()
+    assert v[2, 200] == 0 and s[2, 1] == s[2, 0]
 
 
 # ------------------------------------------------------------------- pack --
