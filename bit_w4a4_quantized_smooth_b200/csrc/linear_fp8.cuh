@@ -17,8 +17,9 @@ namespace svdq {
 // A pair computes 256 x 256 output tiles, visited M-fastest; CTA c holds 128
 // of the tile's x rows and 128 of its w rows, the even CTA issues 2-SM MMAs
 // (M = 256, N = 256, K = 32).
-// Ring: 6 stages of 128 columns of K per CTA (x codes and w codes, 128 rows x
-// 128 bytes each, 128-byte swizzle).  Every fourth stage of a tile also brings
+// Ring: 5 stages of 128 columns of K per CTA (x codes and w codes, 128 rows x
+// 128 bytes each, 128-byte swizzle; a sixth changed nothing: 125.9 against
+// 125.0 us at 4608 x 3072 x 12288).  Every fourth stage of a tile also brings
 // the scale tiles of its 512 columns (this CTA's x rows; all 256 w rows), and
 // the MMA warp copies them into one of two scale regions of tensor memory
 // with three tcgen05.cp per 512 columns; stage j of the four selects byte j of
@@ -29,16 +30,16 @@ namespace svdq {
 // Accumulators: two 128 x 256 fp32 tiles overlap in each CTA's TMEM as in the
 // 4-bit kernel: columns [0, 256) and [192, 448), scales in [448, 480).
 constexpr int kL8Threads = 192, kL8ThreadsFp8 = 320;
-constexpr int kL8Stages = 6;
+constexpr int kL8Stages = 5;
 constexpr int kL8BM = 256, kL8BN = 256, kL8BK = 128;
 constexpr uint32_t kL8ABytes = 16384, kL8BBytes = 16384;
 constexpr uint32_t kL8StageBytes = kL8ABytes + kL8BBytes;
 constexpr uint32_t kL8SfBytes = 512 + 1024;           // a stage's scale tiles
 constexpr uint32_t kL8SfOffset = kL8Stages * kL8StageBytes;
 constexpr uint32_t kL8BiasOffset = kL8SfOffset + kL8Stages * kL8SfBytes;
-constexpr uint32_t kL8OutOffset = kL8BiasOffset + 1024;
-constexpr uint32_t kL8OutBytes = 4096;                // one warp's 32 rows x 128 bytes of output
-constexpr uint32_t kL8BarOffset = kL8OutOffset + 4 * kL8OutBytes;
+constexpr uint32_t kL8OutOffset = (kL8BiasOffset + 2048 + 1023) / 1024 * 1024;
+constexpr uint32_t kL8OutBytes = 4096;                // 32 rows x 128 bytes of output
+constexpr uint32_t kL8BarOffset = kL8OutOffset + 8 * kL8OutBytes;
 constexpr int kL8NumBars = 2 * kL8Stages + 2 + 2 + 1 + 1 + 1;
 constexpr uint32_t kL8TmemCols = 512;
 constexpr uint32_t kL8Acc1Col = 192;
@@ -46,8 +47,7 @@ constexpr uint32_t kL8SfCol = 448;                    // region p: x scales at +
 
 struct L8Params {
   const __nv_bfloat16* bias;
-  uint8_t* y_codes;    // FP8 output [M][N], and its scale tiles
-  uint8_t* y_scales;
+  uint8_t* y_scales;   // FP8 output: scale tiles of the output rows
   int M, K, N;
   int m_tiles, tiles;  // pair tiles: ceil(M / 256) x ceil(N / 256)
   uint64_t timeout_ns;
@@ -55,11 +55,10 @@ struct L8Params {
 
 // FP8_OUT: GELU and FP8 block-128 output.  Two warpgroups of epilogue warps
 // take one 128-column block of the tile each; a thread holds one row's whole
-// block, so the block's scale needs no exchange, and the row's 128 code bytes
-// leave as eight 16-byte stores.  (With four warps for both blocks the
-// epilogue took longer than the MMAs of a 3072-wide tile: 172 us against 153
-// without GELU at 4608 x 3072 x 12288, sustained.)  Otherwise bf16 through a
-// staging block and TMA stores.
+// block, so the block's scale needs no exchange.  Otherwise bf16, one
+// warpgroup.  Both leave through staging blocks and TMA stores (16-byte stores
+// straight from the registers cost 13 us of 161 at 4608 x 3072 x 12288 with
+// FP8 output).  The bias of the next tile is loaded while this one is worked on.
 template <bool FP8_OUT>
 __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     linear_fp8_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -135,31 +134,40 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
       const int nb = (pair / p.m_tiles) * kL8BN + 128 * static_cast<int>(rank);
       for (int it = 0; it < min(total, kL8Stages); ++it) e_tma_prefetch_2d(&tm_w, it * kL8BK, nb);
     }
+    const uint32_t lead_full = lead(full);
     griddep_wait();
-    uint32_t g = 0;
+    // Both issue loops carry slot, phase and addresses along: they share their
+    // schedulers with the epilogue's warps, and a stage is 515 cycles of MMAs.
+    uint32_t g = 0, s = 0, ph = 1;
     bool ok = true;
     for (int t = pair; t < p.tiles && ok && !warp_flag(abort_flag); t += pairs) {
       const int band = (t % p.m_tiles) * 2 + static_cast<int>(rank);  // this CTA's 128 rows
       const int n0 = (t / p.m_tiles) * kL8BN;
-      for (int it = 0; it < total; ++it, ++g) {
-        const int s = g % kL8Stages;
-        ok = warp_wait(smem_u32(&empty[s]), ((g / kL8Stages) & 1) ^ 1, p.timeout_ns, 60);
+      const int nb = n0 + 128 * static_cast<int>(rank);
+      const int x_st = band * band_tiles, w_st = (n0 >> 7) * band_tiles;
+      for (int it = 0; it < total; ++it) {
+        ok = warp_wait(smem_u32(empty) + 8 * s, ph, p.timeout_ns, 60);
         if (!ok) {
           *abort_flag = 1;
           break;
         }
-        const uint32_t fb = lead(&full[s]);
+        const uint32_t fb = lead_full + 8 * s;
         const uint32_t a_s = sbase + s * kL8StageBytes;
-        if (rank == 0) e_arrive_expect_tx(smem_u32(&full[s]), 2 * stage_tx(it));
+        if (rank == 0) e_arrive_expect_tx(smem_u32(full) + 8 * s, 2 * stage_tx(it));
         e_tma_load_2d_pair(a_s, &tm_x, fb, it * kL8BK, band * 128);
-        e_tma_load_2d_pair(a_s + kL8ABytes, &tm_w, fb, it * kL8BK, n0 + 128 * static_cast<int>(rank));
+        e_tma_load_2d_pair(a_s + kL8ABytes, &tm_w, fb, it * kL8BK, nb);
         if ((it & 3) == 0) {
           // bands past the end of a tensor read zeros; their rows are never stored
           const uint32_t sf = sbase + kL8SfOffset + s * kL8SfBytes;
           const int st = it >> 2;
-          e_tma_load_3d_pair(sf, &tm_xs, fb, 0, 0, band * band_tiles + st);
-          e_tma_load_3d_pair(sf + 512, &tm_ws, fb, 0, 0, (n0 >> 7) * band_tiles + st);
-          e_tma_load_3d_pair(sf + 1024, &tm_ws, fb, 0, 0, ((n0 >> 7) + 1) * band_tiles + st);
+          e_tma_load_3d_pair(sf, &tm_xs, fb, 0, 0, x_st + st);
+          e_tma_load_3d_pair(sf + 512, &tm_ws, fb, 0, 0, w_st + st);
+          e_tma_load_3d_pair(sf + 1024, &tm_ws, fb, 0, 0, w_st + band_tiles + st);
+        }
+        ++g;
+        if (++s == kL8Stages) {
+          s = 0;
+          ph ^= 1u;
         }
       }
     }
@@ -190,7 +198,11 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
       // -------------------------------------------------- MMA issuer --
       // E4M3 x E4M3, UE8M0 scales; bits 4-5 and 29-30 select the scale bytes
       const uint32_t idesc = (1u << 23) | ((kL8BN >> 3) << 17) | ((kL8BM >> 4) << 24);
-      uint32_t g = 0, sg = 0;  // stages; scale groups copied
+      const uint64_t a_d0 = make_sdesc(sbase, 16, 1024, 2);
+      const uint64_t b_d0 = make_sdesc(sbase + kL8ABytes, 16, 1024, 2);
+      const uint64_t sf_d0 = make_sdesc(sbase + kL8SfOffset, 0, 128, 0);
+      uint32_t s = 0, ph = 0;
+      uint32_t sft = tmem + kL8SfCol + 16;
       int i = 0;
       bool ok = true;
       for (int t = pair; t < p.tiles && ok && !warp_flag(abort_flag); t += pairs, ++i) {
@@ -200,28 +212,32 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
         if (ok && i >= 1) ok = warp_wait_cluster(smem_u32(ovl_free), (i - 1) & 1, p.timeout_ns, 62);
         if (!ok) break;
         tc_fence_after();
-        for (int it = 0; it < total; ++it, ++g) {
-          const int s = g % kL8Stages;
-          ok = warp_wait(smem_u32(&full[s]), (g / kL8Stages) & 1, p.timeout_ns, 63);
+        uint32_t more = 0;  // the tile's first MMA starts the accumulator
+        for (int it = 0; it < total; ++it) {
+          ok = warp_wait(smem_u32(full) + 8 * s, ph, p.timeout_ns, 63);
           if (!ok) break;
-          const uint32_t a_s = sbase + s * kL8StageBytes;
-          const uint32_t b_s = a_s + kL8ABytes;
           tc_fence_after();
-          if ((it & 3) == 0) {
-            const uint32_t sf = sbase + kL8SfOffset + s * kL8SfBytes;
-            const uint32_t sft = tmem + kL8SfCol + 16 * (sg & 1);
-            e_tmem_cp_pair_32x128b_warpx4(sft, make_sdesc(sf, 0, 128, 0));
-            e_tmem_cp_pair_32x128b_warpx4(sft + 8, make_sdesc(sf + 512, 0, 128, 0));
-            e_tmem_cp_pair_32x128b_warpx4(sft + 12, make_sdesc(sf + 1024, 0, 128, 0));
-            ++sg;
+          const uint64_t a_d = a_d0 + s * (kL8StageBytes >> 4);
+          const uint64_t b_d = b_d0 + s * (kL8StageBytes >> 4);
+          const uint32_t j = static_cast<uint32_t>(it) & 3u;
+          if (j == 0) {
+            const uint64_t sf_d = sf_d0 + s * (kL8SfBytes >> 4);
+            sft ^= (tmem + kL8SfCol) ^ (tmem + kL8SfCol + 16);
+            e_tmem_cp_pair_32x128b_warpx4(sft, sf_d);
+            e_tmem_cp_pair_32x128b_warpx4(sft + 8, sf_d + 32);
+            e_tmem_cp_pair_32x128b_warpx4(sft + 12, sf_d + 64);
           }
-          const uint32_t sft = tmem + kL8SfCol + 16 * ((sg - 1) & 1);
-          const uint32_t id = idesc | (static_cast<uint32_t>(it & 3) << 4) | (static_cast<uint32_t>(it & 3) << 29);
+          const uint32_t id = idesc | (j << 4) | (j << 29);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            e_mma_mxf8_pair(acc, make_sdesc(a_s + kk * 32, 16, 1024, 2), make_sdesc(b_s + kk * 32, 16, 1024, 2), id,
-                            sft, sft + 8, (it > 0 || kk > 0) ? 1u : 0u);
-          e_commit_pair_both(smem_u32(&empty[s]));
+          for (int kk = 0; kk < 4; ++kk) {
+            e_mma_mxf8_pair(acc, a_d + 2 * kk, b_d + 2 * kk, id, sft, sft + 8, more);
+            more = 1;
+          }
+          e_commit_pair_both(smem_u32(empty) + 8 * s);
+          if (++s == kL8Stages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
         e_commit_pair_both(smem_u32(&acc_full[b]));
       }
@@ -235,28 +251,34 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     // ------------------------------------------------------- epilogue --
     griddep_wait();            // the bias and Y may belong to the kernel ahead
     const int wg = FP8_OUT ? (warp - 2) >> 2 : 0;  // FP8 output: the warpgroup's block of the tile
-    const int et = (tid - 64) & 127;
     const int q = warp & 3;    // TMEM lane quadrant this warp may access
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    uint8_t* blk = smem + kL8OutOffset + ((warp - 2) & 3) * kL8OutBytes;  // bf16 output only
-    uint8_t* rowp = blk + lane * 128;
+    uint8_t* out_s = smem + kL8OutOffset + (FP8_OUT ? warp - 2 : 2 * (warp - 2)) * kL8OutBytes;
+    // bias columns of this thread: c0 (and c0 + 128 with one warpgroup)
+    const int c0 = 128 * wg + ((tid - 64) & 127);
+    auto bias_of = [&](int t, int c) {
+      const int n = (t / p.m_tiles) * kL8BN + c;
+      return (p.bias && t < p.tiles && n < N) ? __bfloat162float(p.bias[n]) : 0.0f;
+    };
+    bias_s[c0] = bias_of(pair, c0);
+    if constexpr (!FP8_OUT) bias_s[c0 + 128] = bias_of(pair, c0 + 128);
     int i = 0;
     for (int t = pair; t < p.tiles; t += pairs, ++i) {
       const int b = i & 1;
       const int m0 = ((t % p.m_tiles) * 2 + static_cast<int>(rank)) * 128;
       const int n0 = (t / p.m_tiles) * kL8BN;
-      named_bar_sync(1 + wg, 128);  // everyone is done with the previous tile's bias
-      for (int j = FP8_OUT ? 128 * wg + et : et; j < (FP8_OUT ? 128 * wg + 128 : kL8BN); j += 128) {
-        const int n = n0 + j;
-        bias_s[j] = (p.bias && n < N) ? __bfloat162float(p.bias[n]) : 0.0f;
-      }
-      named_bar_sync(1 + wg, 128);
+      named_bar_sync(1 + wg, 128);  // this tile's bias is there, the one before is done with
+      const float* bias_t = bias_s + kL8BN * b;
+      const float next0 = bias_of(t + pairs, c0);
+      const float next1 = FP8_OUT ? 0.0f : bias_of(t + pairs, c0 + 128);
       // no early exit: the warps of a group must keep meeting its named barrier
       const bool ok = !warp_flag(abort_flag) && warp_wait(smem_u32(&acc_full[b]), (i >> 1) & 1, p.timeout_ns, 70);
       if (!ok) {
         *abort_flag = 1;
         continue;
       }
+      bias_s[kL8BN * (b ^ 1) + c0] = next0;
+      if constexpr (!FP8_OUT) bias_s[kL8BN * (b ^ 1) + c0 + 128] = next1;
       tc_fence_after();
       const uint32_t acc_col = b ? kL8Acc1Col : 0u;
       if constexpr (FP8_OUT) {
@@ -265,7 +287,7 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(src + 32 * j, reinterpret_cast<uint32_t*>(v) + 32 * j);
         tmem_ld_wait();
-        const float* bs = bias_s + 128 * wg;
+        const float* bs = bias_t + 128 * wg;
         const int nb = n0 + 128 * wg;
         const int valid = N - nb;  // columns of the block below N; the others have zero weights and bias, GELU(0) = 0
 #pragma unroll
@@ -277,7 +299,8 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
         // accumulators are read again, 16 columns at a time, before they are
         // released
         const float hi = max_n<128>(v);
-        const bool careful = !(hi > kGeluPos);
+        const int m = m0 + 32 * q + lane;
+        const bool careful = m < p.M && !(hi > kGeluPos);
         const bool any_careful = __any_sync(0xffffffffu, careful);
         if (!any_careful) {
           tc_fence_before();
@@ -314,14 +337,17 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
         }
         const uint32_t sb = fp8_scale_byte(amax);
         const float inv = fp8_inv_scale(sb);
-        const int m = m0 + 32 * q + lane;
-        if (m < p.M) {
-          uint8_t* dst = p.y_codes + static_cast<int64_t>(m) * N + nb;
+        if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
+        __syncwarp();
+        uint8_t* rowp = out_s + lane * 128;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {  // N is a multiple of 16
-            if (16 * j < valid)
-              *reinterpret_cast<uint4*>(dst + 16 * j) = codes16(v + 16 * j, inv);
-          }
+        for (int j = 0; j < 8; ++j)  // 16-byte chunk j = columns 16 j .. 16 j + 15
+          *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = codes16(v + 16 * j, inv);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && valid > 0 && m0 + 32 * q < p.M) {
+          tma_store_2d(&tm_y, smem_u32(out_s), nb, m0 + 32 * q);
+          bulk_commit_group();
         }
         // the block's scale byte; the last tile's second block also writes the
         // rest of the row's last word.  Padding rows of the last 128-row band
@@ -335,19 +361,23 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
 #pragma unroll 1
         for (int gi = 0; gi < 4; ++gi) {
           // 64-column groups; the 64 shared columns ([192, 256)) come first
-          const int c0 = b ? 2 * gi : ((6 + 2 * gi) & 7);  // first 32-column chunk
+          const int g0 = b ? 2 * gi : ((6 + 2 * gi) & 7);  // first 32-column chunk
           uint32_t v[64];
-          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * c0, v);
-          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * c0 + 32, v + 32);
+          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * g0, v);
+          tmem_ld_32x32b_x32(tmem + lane_base + acc_col + 32 * g0 + 32, v + 32);
           tmem_ld_wait();
           if (gi == 0 || gi == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(lead(gi == 0 ? ovl_free : &acc_empty[b]));
           }
-          if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
+          // the staging block (alternating per group) must no longer be read
+          // by this warp's last store but one
+          uint8_t* blk = out_s + (gi & 1) * kL8OutBytes;
+          uint8_t* rowp = blk + lane * 128;
+          if (lane == 0) bulk_wait_group_read<1>();
           __syncwarp();
-          const float* bs = bias_s + 32 * c0;
+          const float* bs = bias_t + 32 * g0;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {  // 16-byte chunk j = columns 8 j .. 8 j + 7
             auto y = [&](int e) { return __uint_as_float(v[8 * j + e]) + bs[8 * j + e]; };
@@ -357,8 +387,8 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && n0 + 32 * c0 < N && m0 + 32 * q < p.M) {
-            tma_store_2d(&tm_y, smem_u32(blk), n0 + 32 * c0, m0 + 32 * q);
+          if (lane == 0 && n0 + 32 * g0 < N && m0 + 32 * q < p.M) {
+            tma_store_2d(&tm_y, smem_u32(blk), n0 + 32 * g0, m0 + 32 * q);
             bulk_commit_group();
           }
         }

@@ -552,7 +552,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (svdq_status rc = fp8_scales_map(&tm_xs, x_scales, M, K)) return rc;
   if (svdq_status rc = fp8_scales_map(&tm_ws, w_scales, N, K)) return rc;
   if (fp8_out) {
-    std::memset(&tm_y, 0, sizeof(tm_y));  // codes are stored from registers
+    if (svdq_status rc = fp8_codes_map(&tm_y, Y, M, N, 32)) return rc;  // one epilogue warp's 32 x 128 block
   } else {
     const uint64_t dims[2] = {static_cast<uint64_t>(N), static_cast<uint64_t>(M)};
     const uint64_t strides[1] = {static_cast<uint64_t>(N) * 2};
@@ -563,7 +563,6 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   }
   svdq::L8Params p;
   p.bias = static_cast<const __nv_bfloat16*>(bias);
-  p.y_codes = fp8_out ? static_cast<uint8_t*>(Y) : nullptr;
   p.y_scales = y_scales;
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
