@@ -50,6 +50,7 @@ struct L8Params {
   uint8_t* y_scales;   // FP8 output: scale tiles of the output rows
   int M, K, N;
   int m_tiles, tiles;  // pair tiles: ceil(M / 256) x ceil(N / 256)
+  int one;             // 1 (see the FP8 epilogue)
   uint64_t timeout_ns;
 };
 
@@ -287,75 +288,72 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(src + 32 * j, reinterpret_cast<uint32_t*>(v) + 32 * j);
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (wg != b) mbar_arrive_remote(lead(ovl_free));  // this block holds the 64 shared columns
+          mbar_arrive_remote(lead(&acc_empty[b]));
+        }
         const float* bs = bias_t + 128 * wg;
         const int nb = n0 + 128 * wg;
         const int valid = N - nb;  // columns of the block below N; the others have zero weights and bias, GELU(0) = 0
-#pragma unroll
-        for (int j = 0; j < 128; j += 2) {
-          float2 c = *reinterpret_cast<const float2*>(bs + j);
-          add2_rn(v[j], v[j + 1], v[j], v[j + 1], c.x, c.y);
-        }
-        // a row without an x above 0.3 needs more care (fp8.cuh): then its
-        // accumulators are read again, 16 columns at a time, before they are
-        // released
-        const float hi = max_n<128>(v);
         const int m = m0 + 32 * q + lane;
-        const bool careful = m < p.M && !(hi > kGeluPos);
-        const bool any_careful = __any_sync(0xffffffffu, careful);
-        if (!any_careful) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (wg != b) mbar_arrive_remote(lead(ovl_free));  // this block holds the 64 shared columns
-            mbar_arrive_remote(lead(&acc_empty[b]));
+        // Always taken, but the compiler does not know: in one straight line it
+        // moves the arithmetic ahead of the arrivals above, and the next
+        // tile's MMAs wait for it (157 against 135 us at 4608 x 3072 x 12288 on
+        // B200).
+        if (p.one) {
+#pragma unroll
+          for (int j = 0; j < 128; j += 2) {
+            const float2 c = *reinterpret_cast<const float2*>(bs + j);
+            add2_rn(v[j], v[j + 1], v[j], v[j + 1], c.x, c.y);
           }
-        }
+          // a row without an x above 0.3 needs more care (fp8.cuh)
+          const float hi = max_n<128>(v);
+          const bool careful = m < p.M && !(hi > kGeluPos);
+          float top[2] = {hi, 0.0f};
+          gelu_fast<2>(top);
+          float amax = top[0];
+          if (!__any_sync(0xffffffffu, careful)) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 16) gelu_fast<16>(v + j);
-        float top[2] = {hi, 0.0f};
-        gelu_fast<2>(top);
-        float amax = top[0];
-        if (any_careful) {
+            for (int j = 0; j < 128; j += 16) gelu_fast<16>(v + j);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 128; j += 16) {
-            uint32_t w[16];
-            tmem_ld_32x32b_x16(src + j, w);
-            tmem_ld_wait();
+            for (int j = 0; j < 128; j += 16) {
+              float x[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __uint_as_float(w[e]) + bs[j + e];
-              if (careful && x < -kGeluFast) v[j + e] = gelu_tail(x);
+              for (int e = 0; e < 16; ++e) x[e] = v[j + e];
+              gelu_fast<16>(v + j);
+              if (careful) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (x[e] < -kGeluFast) v[j + e] = gelu_tail(x[e]);
+              }
             }
+            if (careful) amax = amax_n<128>(v);
           }
-          tc_fence_before();
+          const uint32_t sb = fp8_scale_byte(amax);
+          const float inv = fp8_inv_scale(sb);
+          if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
           __syncwarp();
-          if (lane == 0) {
-            if (wg != b) mbar_arrive_remote(lead(ovl_free));
-            mbar_arrive_remote(lead(&acc_empty[b]));
-          }
-          if (careful) amax = amax_n<128>(v);
-        }
-        const uint32_t sb = fp8_scale_byte(amax);
-        const float inv = fp8_inv_scale(sb);
-        if (lane == 0) bulk_wait_group_read<0>();  // this warp's previous store has read the block
-        __syncwarp();
-        uint8_t* rowp = out_s + lane * 128;
+          uint8_t* rowp = out_s + lane * 128;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)  // 16-byte chunk j = columns 16 j .. 16 j + 15
-          *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = codes16(v + 16 * j, inv);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && valid > 0 && m0 + 32 * q < p.M) {
-          tma_store_2d(&tm_y, smem_u32(out_s), nb, m0 + 32 * q);
-          bulk_commit_group();
-        }
-        // the block's scale byte; the last tile's second block also writes the
-        // rest of the row's last word.  Padding rows of the last 128-row band
-        // get zeros.
-        if (m0 < p.M) {
-          uint8_t* dst = p.y_scales + fp8_scale_offset(m, nb >> 7, fp8_band_tiles(N));
-          *dst = m < p.M ? static_cast<uint8_t>(sb) : uint8_t{0};
-          if (wg == 1 && ((n0 >> 8) & 1) == 0 && n0 + kL8BN >= N) *reinterpret_cast<uint16_t*>(dst + 1) = 0;
+          for (int j = 0; j < 8; ++j)  // 16-byte chunk j = columns 16 j .. 16 j + 15
+            *reinterpret_cast<uint4*>(rowp + ((j ^ (lane & 7)) << 4)) = codes16(v + 16 * j, inv);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && valid > 0 && m0 + 32 * q < p.M) {
+            tma_store_2d(&tm_y, smem_u32(out_s), nb, m0 + 32 * q);
+            bulk_commit_group();
+          }
+          // the block's scale byte; the last tile's second block also writes the
+          // rest of the row's last word.  Padding rows of the last 128-row band
+          // get zeros.
+          if (m0 < p.M) {
+            uint8_t* dst = p.y_scales + fp8_scale_offset(m, nb >> 7, fp8_band_tiles(N));
+            *dst = m < p.M ? static_cast<uint8_t>(sb) : uint8_t{0};
+            if (wg == 1 && ((n0 >> 8) & 1) == 0 && n0 + kL8BN >= N) *reinterpret_cast<uint16_t*>(dst + 1) = 0;
+          }
         }
       } else {
 #pragma unroll 1

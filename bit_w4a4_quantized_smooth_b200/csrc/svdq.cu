@@ -567,6 +567,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
   p.N = static_cast<int>(N);
+  p.one = 1;
   p.m_tiles = static_cast<int>((M + svdq::kL8BM - 1) / svdq::kL8BM);
   p.tiles = p.m_tiles * static_cast<int>((N + svdq::kL8BN - 1) / svdq::kL8BN);
   p.timeout_ns = wait_timeout_ns();
