@@ -61,7 +61,7 @@ def build_torch_calls() -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     cmd += [f"-I{d}" for d in inc if os.path.isdir(d)]
     cmd += [TORCH_SOURCE, "-o", TORCH_LIB + ".tmp"] + [f"-L{d}" for d in library_paths()]
-    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-L{HERE}", "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN"]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-L{HERE}", "-l:libsvdq.so", "-Wl,-rpath,$ORIGIN"]
     subprocess.check_call(cmd, cwd=CSRC)
     os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     return TORCH_LIB

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -118,7 +119,7 @@ void run(const char* what, at::Device dev, const StreamArg& s, F&& f) {
 }
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::detail::empty_cuda(shape, type, dev, std::nullopt);  // past the dispatcher
 }
 
 // Codes and scales of [rows][K]: given ones are checked here, missing ones are made by fill().

@@ -65,7 +65,7 @@ def _act(rng, M, K):
 
 # --------------------------------------------------------------- quantise --
 SHAPES = [(1, 16), (1, 128), (3, 112), (5, 144), (33, 512), (127, 528), (128, 640), (129, 1040), (300, 2064),
-          (2, 12288)]
+          (2, 12288), (9477, 528), (1301, 4112)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -190,7 +190,7 @@ def test_pack_weight_bit_exact(K, N, dt):
 
 # ------------------------------------------------------------------- norm --
 @pytest.mark.parametrize("M,K", [(1, 16), (1, 3072), (2, 128), (5, 144), (129, 528), (64, 4112), (3, 8208), (2, 16384),
-                                 (1, 32768)])
+                                 (1, 32768), (1300, 528), (1203, 3072), (400, 8208), (2, 20016)])
 @pytest.mark.parametrize("res", ["none", "bf16", "f32"])
 @pytest.mark.parametrize("gamma", [True, False])
 def test_rmsnorm(M, K, res, gamma):
