@@ -102,10 +102,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // 12288).  The coefficients are this project's own fit: minimax in g
 // (reweighted least squares on Chebyshev nodes, |error| 1.3e-7 in ln Phi),
 // rounded to fp32.
-// Beyond 5.5 it clamps z: for x > 5.5 that is right to the last bit (the
-// last step rounds toward zero: the exact result lies below x by less than
-// half an ulp, and rounding up to x would turn an E4M3 tie the wrong way); for
-// x < -5.5 it gives -1.05e-7 for a result between that and 0.  In a block
+// Beyond 5.5 it clamps z: for x > 5.5 that is right to the last bit (with
+// TIES, for inputs that are bf16 and so often E4M3 ties themselves, the last
+// step rounds toward zero: the exact result lies below x by less than half an
+// ulp, and rounding up to x would turn the tie the wrong way); for x < -5.5 it gives -1.05e-7 for a result between that and 0.  In a block
 // whose largest result is 0.1 or more both get the code -0 (half the smallest
 // step is 2^-10 2^-12 = 2.4e-7), so gelu_tail is needed only in a block
 // without any x above 0.3 (GELU(0.3) = 0.185).  Where there is one, it also
@@ -129,7 +129,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // n values (n even), coefficient by coefficient: the n / 2 chains of packed
 // operations are independent, and a coefficient's register pair is set once
 // for all of them.
-template <int n>
+template <int n, bool TIES>
 __device__ __forceinline__ void gelu_fast(float* x) {
   constexpr float c[11] = {-0.9999998211860657f,    1.1511125564575195f,    -0.4591609537601471f,
                            0.05260409042239189f,    0.007166661322116852f,  0.00016647009761072695f,
@@ -154,9 +154,9 @@ __device__ __forceinline__ void gelu_fast(float* x) {
   for (int i = 0; i < n / 2; ++i) {
     float g0, g1;
     unpack_f32x2(g[i], g0, g1);
-    unpack_f32x2(fma_rz_f32x2(nz[i], pack_f32x2(ex2_approx_ftz(g0), ex2_approx_ftz(g1)),
-                              pack_f32x2(fmaxf(x[2 * i], 0.0f), fmaxf(x[2 * i + 1], 0.0f))),
-                 x[2 * i], x[2 * i + 1]);
+    const uint64_t phi = pack_f32x2(ex2_approx_ftz(g0), ex2_approx_ftz(g1));
+    const uint64_t pos = pack_f32x2(fmaxf(x[2 * i], 0.0f), fmaxf(x[2 * i + 1], 0.0f));
+    unpack_f32x2(TIES ? fma_rz_f32x2(nz[i], phi, pos) : fma_f32x2(nz[i], phi, pos), x[2 * i], x[2 * i + 1]);
   }
 }
 
@@ -203,12 +203,12 @@ __device__ __forceinline__ float max_n(const float* v) {
 
 // GELU of this lane's n values (n even) of a block spread over `lanes`
 // neighbouring lanes, and the block's largest magnitude.  All lanes call it.
-template <int n, int lanes>
+template <int n, int lanes, bool TIES>
 __device__ __forceinline__ float gelu_block(float* v) {
   float x[n];
 #pragma unroll
   for (int i = 0; i < n; ++i) x[i] = v[i];
-  gelu_fast<n>(v);
+  gelu_fast<n, TIES>(v);
   float a = max_n<n>(v);
 #pragma unroll
   for (int o = lanes / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -320,7 +320,7 @@ __device__ __forceinline__ void zero_pad_scales(uint8_t* scales, int64_t M, int6
 __device__ __forceinline__ void store_gelu_fp8(float* v, uint8_t* codes, uint8_t* scales, int64_t m, int n, int N,
                                                int lane) {
   if (n >= N) v[0] = v[1] = v[2] = v[3] = 0.0f;  // GELU(0) = 0
-  const float a = gelu_block<4, 32>(v);
+  const float a = gelu_block<4, 32, false>(v);
   const uint32_t b = fp8_scale_byte(a);
   const float inv = fp8_inv_scale(b);
   if (n < N)
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kQ8Threads)
     }
     float a;
     if constexpr (GELU) {
-      a = gelu_block<16, 8>(v);
+      a = gelu_block<16, 8, true>(v);
     } else {
       a = amax_n<16>(v);
 #pragma unroll

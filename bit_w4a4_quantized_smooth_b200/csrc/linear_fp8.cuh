@@ -312,18 +312,18 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
           const float hi = max_n<128>(v);
           const bool careful = m < p.M && !(hi > kGeluPos);
           float top[2] = {hi, 0.0f};
-          gelu_fast<2>(top);
+          gelu_fast<2, false>(top);
           float amax = top[0];
           if (!__any_sync(0xffffffffu, careful)) {
 #pragma unroll
-            for (int j = 0; j < 128; j += 16) gelu_fast<16>(v + j);
+            for (int j = 0; j < 128; j += 16) gelu_fast<16, false>(v + j);
           } else {
 #pragma unroll
             for (int j = 0; j < 128; j += 16) {
               float x[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = v[j + e];
-              gelu_fast<16>(v + j);
+              gelu_fast<16, false>(v + j);
               if (careful) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
