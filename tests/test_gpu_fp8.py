@@ -524,3 +524,142 @@ def test_binding_refusals_on_the_device():
         with pytest.raises(svdq.SvdqError):
             call()
     _ok()
+
+
+# -------------------------------------------------- what is easily missed --
+def test_first_call_of_a_process_inside_a_capture():
+    """No call needs a warm-up: attributes, maps and plans are set up on the host."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import bit_w4a4_quantized_smooth_b200 as svdq
+X = torch.randn(4, 512, device="cuda").bfloat16()
+W = torch.randn(512, 256, device="cuda").bfloat16()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    wc, ws = svdq.pack_weight_fp8(W)
+    xc, xs, _, _ = svdq.rmsnorm(X)
+    hc, hs = svdq.linear_fp8_gelu(xc, xs, wc, ws)
+    qc, qs = svdq.quantize_fp8(X)
+    y = svdq.linear_fp8(qc, qs, wc, ws)
+g.replay()
+torch.cuda.synchronize()
+assert svdq.sync_status()[0] == 0
+assert torch.equal(y, svdq.linear_fp8(*svdq.quantize_fp8(X), *svdq.pack_weight_fp8(W)))
+a = svdq.linear_fp8_gelu(*svdq.rmsnorm(X)[:2], *svdq.pack_weight_fp8(W))
+assert torch.equal(hc.view(torch.uint8), a[0].view(torch.uint8))
+print("captured")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of X, of the weights and of their codes that start past 2^32 bytes."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(2)
+    ld, M, K = 600_000, 4100, 528                              # 4.9 GB of bf16
+    big = torch.zeros((M, ld), dtype=torch.bfloat16, device="cuda")
+    X = big[:, ld - K:]
+    rows = [0, 1, 1789, 1790, 3579, 3580, M - 1]
+    v = torch.from_numpy(rng.normal(size=(len(rows), K))).to(torch.bfloat16).cuda()
+    X[rows] = v
+    codes, scales = svdq.quantize_fp8(X)
+    c, s = ref.encode(_np(v))
+    assert np.array_equal(_np(codes[rows]), c)
+    assert np.array_equal(ref.untile(_np(scales), M, K)[0][rows], s)
+    want = svdq.rmsnorm(v, bf16_out=True)[3]
+    assert torch.equal(svdq.rmsnorm(X, bf16_out=True)[3][rows], want)
+    del big, X
+    K, N = 4112, 1_048_560                                     # 4.3 GB of codes, 8.6 GB of bf16 weights
+    W = torch.zeros((K, N), dtype=torch.bfloat16, device="cuda")
+    cols = torch.tensor([0, 7, 522_301, 1_044_480, 1_044_481, N - 1])
+    w = torch.from_numpy(rng.normal(size=(K, len(cols)))).to(torch.bfloat16).cuda()
+    W[:, cols.cuda()] = w
+    wc, ws = svdq.pack_weight_fp8(W)
+    _ok()
+    del W
+    c, s = ref.encode(np.ascontiguousarray(_np(w).T))
+    assert np.array_equal(_np(wc.view(torch.uint8)[cols.cuda()]), c)
+    x = torch.from_numpy(rng.normal(size=(3, K))).to(torch.bfloat16).cuda()
+    xc, xs = svdq.quantize_fp8(x)
+    xv = ref.decode(_np(xc), ref.untile(_np(xs), 3, K)[0])
+    wv = ref.decode(c, s)
+    y, E = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    for path in ("large", "small"):
+        svdq.set_linear_fp8_path(path)
+        try:
+            Y = svdq.linear_fp8(xc, xs, wc, ws)
+            gc, gs = svdq.linear_fp8_gelu(xc, xs, wc, ws)
+        finally:
+            svdq.set_linear_fp8_path("auto")
+        _ok()
+        _check_y(Y[:, cols.cuda()], y, (-(-K // 32) + 1) * 2.0 ** -23 * E)
+        others = torch.ones(N, dtype=torch.bool, device="cuda")
+        others[cols.cuda()] = False
+        assert (Y[:, others] == 0).all()
+        g = ref.gelu(y)
+        top = _np(gc[:, cols.cuda()])
+        sb = ref.untile(_np(gs), 3, N)[0][:, (cols // 128).numpy()]
+        got = ref.E4M3[top] * np.exp2(sb.astype(np.float64) - 127)
+        assert (np.abs(got - g) <= np.abs(g) * 0.0626 + 2.0 ** -10 * np.exp2(sb.astype(np.float64) - 127)).all()
+
+
+def test_unaligned_rows_take_the_16_byte_path():
+    """Row strides and starts that are multiples of 16 bytes but not of 32."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(8)
+    W = _dev(rng.normal(size=(70, 1048)), torch.bfloat16)
+    R = _dev(rng.normal(size=(70 * 528 + 8,)), torch.float32)
+    for start in (0, 8, 24):
+        X = W[:, start:start + 528]
+        c, s = ref.encode(_np(X))
+        codes, scales = svdq.quantize_fp8(X)
+        assert np.array_equal(_np(codes), c) and np.array_equal(_np(scales), ref.tiles(s))
+        for res in (None, R[4:4 + 70 * 528].view(70, 528), R[:70 * 528].view(70, 528)):
+            a = svdq.rmsnorm(X, None, res, bf16_out=True)
+            b = svdq.rmsnorm(X.contiguous(), None, None if res is None else res.clone(), bf16_out=True)
+            assert all(torch.equal(p, q) for p, q in zip(a[2:], b[2:]) if p is not None)
+            assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8))
+    _ok()
+
+
+def test_zero_rows_with_eps_zero_are_nan():
+    torch, svdq = _m()
+    X = torch.zeros((2, 256), dtype=torch.bfloat16, device="cuda")
+    X[1] = 2.0
+    codes, scales, _, Y = svdq.rmsnorm(X, eps=0.0, bf16_out=True)
+    _ok()
+    assert torch.isnan(Y[0]).all() and torch.isnan(codes.float()[0]).all() and (Y[1] == 1).all()
+
+
+def test_two_threads_call_at_once():
+    """Plans, maps and attributes are shared by the process's threads."""
+    import threading
+    torch, svdq = _m()
+    rng = np.random.default_rng(21)
+    L = _mlp_weights(svdq, torch, rng, 512, 1040)
+    Xs = [_dev(rng.normal(size=(m, 512)), torch.bfloat16) for m in (3, 17, 90, 200)]
+    want = [_mlp(svdq, L, x, torch.zeros_like(x)) for x in Xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for i in range(20):
+                    j = (i + k) % len(Xs)
+                    if not torch.equal(_mlp(svdq, L, Xs[j], torch.zeros_like(Xs[j])), want[j]):
+                        bad.append((k, i))
+        except Exception as e:  # noqa: BLE001
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work, args=(k,)) for k in range(3)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad, bad[:3]
+    _ok()
