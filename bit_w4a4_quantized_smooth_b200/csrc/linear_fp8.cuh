@@ -147,16 +147,15 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
       const int nb = n0 + 128 * static_cast<int>(rank);
       const int x_st = band * band_tiles, w_st = (n0 >> 7) * band_tiles;
       for (int it = 0; it < total; ++it) {
-        ok = warp_wait(smem_u32(empty) + 8 * s, ph, p.timeout_ns, 60);
+        ok = warp_wait_ready(smem_u32(empty) + 8 * s, ph, p.timeout_ns, 60);
         if (!ok) {
           *abort_flag = 1;
           break;
         }
         const uint32_t fb = lead_full + 8 * s;
         const uint32_t a_s = sbase + s * kL8StageBytes;
-        if (rank == 0) e_arrive_expect_tx(smem_u32(full) + 8 * s, 2 * stage_tx(it));
-        e_tma_load_2d_pair(a_s, &tm_x, fb, it * kL8BK, band * 128);
-        e_tma_load_2d_pair(a_s + kL8ABytes, &tm_w, fb, it * kL8BK, nb);
+        e_stage_load_pair(fb, rank ^ 1u, smem_u32(full) + 8 * s, 2 * stage_tx(it), a_s, &tm_x, band * 128,
+                          a_s + kL8ABytes, &tm_w, nb, it * kL8BK);
         if ((it & 3) == 0) {
           // bands past the end of a tensor read zeros; their rows are never stored
           const uint32_t sf = sbase + kL8SfOffset + s * kL8SfBytes;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
         tc_fence_after();
         uint32_t more = 0;  // the tile's first MMA starts the accumulator
         for (int it = 0; it < total; ++it) {
-          ok = warp_wait(smem_u32(full) + 8 * s, ph, p.timeout_ns, 63);
+          ok = warp_wait_ready(smem_u32(full) + 8 * s, ph, p.timeout_ns, 63);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a_d = a_d0 + s * (kL8StageBytes >> 4);
@@ -229,12 +228,8 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
             e_tmem_cp_pair_32x128b_warpx4(sft + 12, sf_d + 64);
           }
           const uint32_t id = idesc | (j << 4) | (j << 29);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            e_mma_mxf8_pair(acc, a_d + 2 * kk, b_d + 2 * kk, id, sft, sft + 8, more);
-            more = 1;
-          }
-          e_commit_pair_both(smem_u32(empty) + 8 * s);
+          e_stage_mxf8_pair(acc, a_d, b_d, id, sft, sft + 8, more, smem_u32(empty) + 8 * s);
+          more = 1;
           if (++s == kL8Stages) {
             s = 0;
             ph ^= 1u;

@@ -106,22 +106,22 @@ __global__ void __launch_bounds__(kS8Threads)
     const uint8_t* w_sf = p.w_scales + static_cast<size_t>(n0 >> 7) * band_tiles * 512;
     const uint8_t* x_sf = p.x_scales + static_cast<size_t>(m0 >> 7) * band_tiles * 512;
     griddep_wait();
-    // The loops of both issuing warps carry their slot, phase and addresses
-    // along: with a division by the ring depth and a look at the abort flag a
-    // stage, the instructions of a 16 KB stage took longer than its bytes
-    // (0.38 us a stage on B200, whatever the depth).
+    // The loops of both issuing warps are as short as they get: slot, phase and
+    // addresses carried along, one election and one vote a stage.  With a
+    // division by the ring depth, a look at the abort flag and an election for
+    // each instruction, a 16 KB stage took 0.38 us on B200 whatever the depth
+    // and whatever its bytes.
     int issued = 0;
     uint32_t s = 0, ph = 1, fb = smem_u32(full), eb = smem_u32(empty), w_s = sbase;
     bool ok = true;
     for (int ks = ks0; ks < ks0 + total; ++ks) {
-      if (issued >= S && !warp_wait(eb, ph, p.timeout_ns, 80)) {
+      if (issued >= S && !warp_wait_ready(eb, ph, p.timeout_ns, 80)) {
         ok = false;
         break;
       }
       const bool sf = issued == 0 || (ks & 3) == 0;  // the scale tiles of a new group of 512 columns
-      e_arrive_expect_tx(fb, kS8WBytes + x_bytes + (sf ? kS8SfBytes : 0u));
-      e_tma_load_2d(w_s, &tm_w, fb, ks * kS8BK, n0);
-      e_tma_load_2d(w_s + kS8WBytes, &tm_x, fb, ks * kS8BK, m0);
+      e_stage_load(fb, kS8WBytes + x_bytes + (sf ? kS8SfBytes : 0u), w_s, &tm_w, n0, w_s + kS8WBytes, &tm_x, m0,
+                   ks * kS8BK);
       if (sf) {
         const uint32_t sf_s = w_s + kS8WBytes + x_bytes;
         e_bulk_load(sf_s, w_sf + static_cast<size_t>(ks >> 2) * 512, 512u, fb);
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kS8Threads)
     uint32_t more = 0;  // the first MMA starts the accumulator
     bool ok = true;
     for (int ks = ks0; ks < ks0 + total; ++ks) {
-      ok = warp_wait(fb, ph, p.timeout_ns, 82);
+      ok = warp_wait_ready(fb, ph, p.timeout_ns, 82);
       if (!ok) break;
       tc_fence_after();
       const uint32_t j = static_cast<uint32_t>(ks) & 3u;
@@ -171,12 +171,8 @@ __global__ void __launch_bounds__(kS8Threads)
         e_tmem_cp_32x128b_warpx4(sft + 8, sf_d0 + at + 32);
       }
       const uint32_t id = idesc | (j << 4) | (j << 29);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        e_mma_mxf8(tmem, w_d0 + at + 2 * kk, x_d0 + at + 2 * kk, id, sft, sft + 8, more);
-        more = 1;
-      }
-      e_commit(eb);
+      e_stage_mxf8(tmem, w_d0 + at, x_d0 + at, id, sft, sft + 8, more, eb);
+      more = 1;
       ++s;
       fb += 8;
       eb += 8;
