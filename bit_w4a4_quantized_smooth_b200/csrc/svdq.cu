@@ -392,18 +392,18 @@ int s8_active(int splits, size_t smem, int sms) {
 
 // The split of K and the ring depth with the least estimated time.  The
 // estimate was fitted on B200 to the times of every split from 1 to 8 and
-// depth from 2 to 8 at 60 sizes (M 1 to 256, K 256 to 12288, N 512 to 12288;
-// weights from HBM, launches back to back): with x = bm / 128 and `occ` CTAs
+// depth from 2 to 8, and of the large-M kernel, at 140 sizes (M 1 to 2048, K
+// 256 to 12288, N 512 to 12288; weights from HBM, launches back to back), for
+// the choice rather than for the time itself: with x = bm / 128 and `occ` CTAs
 // on an SM,
-//   0.64 + 2.2 x us            launch, start, epilogue
-//   + 1.4 with a cluster, + 0.8 per 100 CTAs (cluster launch and exchange)
-//   + waves spc max(0.37, 1.2 (1 + 0.92 x) / depth, (0.13 + 0.29 x) occ)
-//                              a stage: an SM's TMA unit brings 16 KB of
-//                              lines that miss L2 in about 0.3 us; the latency
-//                              of a load over the ring's depth
-//   + 3.1 (waves - 1)          clusters that do not fit at once
-// Its choice costs 1.3 % over the best one on average, 9.5 % at the worst.
-// The deeper ring on ties.
+//   2.0 + 0.97 x us            launch, start, epilogue
+//   + 1.9 with a cluster, + 0.37 per 100 CTAs (cluster launch and exchange)
+//   + waves spc max(0.21, 0.71 (1 + 1.3 x) / depth, (0.097 + 0.13 x) occ)
+//                              a stage: its issue; the latency of a load over
+//                              the ring's depth; the SM's share of its loads
+//   + 2.0 (waves - 1)          clusters that do not fit at once
+// Against the best of all measured, its choice (of the kernel as well) costs
+// 0.5 % on average and 8 % at the worst.  The deeper ring on ties.
 svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
@@ -418,7 +418,7 @@ svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t
   for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
     const int spc = (k_stages + s - 1) / s;
     if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
-    for (int depth = std::min(spc, 3); depth <= std::min(spc, 6); ++depth) {
+    for (int depth = std::min(spc, 3); depth <= std::min(spc, 8); ++depth) {
       const uint32_t ring = std::max<uint32_t>(depth * stage, static_cast<uint32_t>(bm) * svdq::kS8BN * 4);
       const size_t smem = smem_for_tmem(dev, 1024 + svdq::kS8HeadBytes + ring, tmem_cols);
       if (smem == 0 || smem > svdq::kS8SmemLimit) continue;
@@ -427,8 +427,8 @@ svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t
       const double ctas = static_cast<double>(tiles) * s;
       const double waves = std::ceil(ctas / active);
       const double occ = std::max(1.0, std::min<double>(ctas, active) / sms);
-      const double per = std::max({0.37, 1.2 * (1.0 + 0.92 * x) / depth, (0.13 + 0.29 * x) * occ});
-      const double us = 0.64 + 2.2 * x + (s > 1 ? 1.4 : 0.0) + 0.008 * ctas + waves * spc * per + 3.1 * (waves - 1) -
+      const double per = std::max({0.21, 0.71 * (1.0 + 1.3 * x) / depth, (0.097 + 0.13 * x) * occ});
+      const double us = 2.0 + 0.97 * x + (s > 1 ? 1.9 : 0.0) + 0.0037 * ctas + waves * spc * per + 2.0 * (waves - 1) -
                         0.02 * depth;
       if (best.splits == 0 || us < best.us) best = {bm, s, spc, depth, tmem_cols, smem, us};
     }
@@ -530,11 +530,11 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (dev < 0) return SVDQ_ERR_CUDA;
   const int sms = sm_count(dev);
   if (sms < 2) return SVDQ_ERR_CUDA;
-  // The few-rows kernel where its estimate is below the large-M kernel's,
-  // 5.2 us + 0.32 us a stage of 128 columns for every wave of CTA pairs
-  // (measured on B200: 13.2 us against 8.2 at 128 x 3072 x 3072, 35.7 against
-  // 18.1 at 256 x 12288 x 3072, but 15.1 against 16.1 at 256 x 3072 x 12288
-  // and 15.5 against 15.9 at 512 x 3072 x 9216).
+  // The few-rows kernel where its estimate is below the large-M kernel's, 4.5
+  // us + (0.30 a stage of 128 columns + 0.75) for every wave of CTA pairs
+  // (measured on B200: 12.2 us against 8.0 at 128 x 3072 x 3072, 33.6 against
+  // 17.6 at 256 x 12288 x 3072 and 28.0 at 512, but 14.2 against 15.8 at 256 x
+  // 3072 x 12288 and 14.4 against 14.9 at 512 x 3072 x 9216).
   const int64_t pair_tiles = ((M + svdq::kL8BM - 1) / svdq::kL8BM) * ((N + svdq::kL8BN - 1) / svdq::kL8BN);
   const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
   const int path = g_linear8_path.load(std::memory_order_relaxed);
@@ -543,7 +543,8 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
                                : reinterpret_cast<const void*>(svdq::linear_fp8_splitk_kernel<false>);
     S8Plan pl;
     if (svdq_status rc = s8_plan_kept(&pl, kern, M, K, N, dev, sms)) return rc;
-    if (path == 2 || pl.us < 5.2 + 0.32 * static_cast<double>(pair_waves * ((K + svdq::kL8BK - 1) / svdq::kL8BK)))
+    const double stages = static_cast<double>((K + svdq::kL8BK - 1) / svdq::kL8BK);
+    if (path == 2 || pl.us < 4.5 + static_cast<double>(pair_waves) * (0.30 * stages + 0.75))
       return fp8_out ? launch_s8<true>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, stream)
                      : launch_s8<false>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, stream);
   }
