@@ -122,6 +122,24 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);  // past the dispatcher
 }
 
+// Two tensors of one-byte elements in one allocation (the second from a
+// multiple of 256 bytes on): an allocation and its release less.
+void make_pair(Opt& a, at::IntArrayRef a_shape, at::ScalarType a_type, Opt& b, int64_t b_len, at::ScalarType b_type,
+               at::Device dev) {
+  const int64_t at_b = (c10::multiply_integers(a_shape) + 255) / 256 * 256;
+  const at::Tensor both = make({at_b + b_len}, at::kByte, dev);
+  auto part = [&](int64_t offset, at::IntArrayRef shape, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(both.storage()),
+                                                            c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    return t;
+  };
+  a = part(0, a_shape, a_type);
+  b = part(at_b, {b_len}, b_type);
+}
+
 // Codes and scales of [rows][K]: given ones are checked here, missing ones are made by fill().
 struct Fp8Out {
   int64_t rows, K;
@@ -133,6 +151,7 @@ struct Fp8Out {
     if (scales) need(*scales, sn, kScales, at::kByte, {scales_len(rows, K)}, dev);
   }
   void fill() {
+    if (!codes && !scales) make_pair(codes, {rows, K}, kCodes, scales, scales_len(rows, K), kScales, dev);
     if (!codes) codes = make({rows, K}, kCodes, dev);
     if (!scales) scales = make({scales_len(rows, K)}, kScales, dev);
   }
