@@ -259,9 +259,10 @@ def channel_absmax(X, amax=None, stream=None):
 # float8_e8m0fnu, flat, in the tile layout of include/svdq.h (uint8 tensors of
 # the same sizes are taken as well).  Types, shapes, strides and devices are
 # checked (ValueError) in the native module _svdq_torch (csrc/torch_calls.cpp),
-# which allocates the outputs that are not given and makes the C ABI's call on
-# the device of the first argument, on that device's current stream unless one
-# is given.
+# which allocates the outputs that are not given (on the stream that writes
+# them; codes and scales share an allocation) and makes the C ABI's call on the
+# device of the first argument, on that device's current stream unless one is
+# given.  Forward only: no gradients are recorded.
 
 _ext = None
 

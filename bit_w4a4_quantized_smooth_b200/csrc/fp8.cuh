@@ -91,7 +91,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // ---------------------------------------------------------------- GELU ----
 // GELU(x) = x Phi(x) = max(x, 0) - |x| Phi(-|x|), which has no cancellation
-// for negative x: about 1e-6 relative, also where the result is small (each
+// for negative x: within 2^-18 relative, also where the result is small (each
 // value keeps its own E4M3 exponent, so an error against the block's largest
 // value would not do).
 //
@@ -102,14 +102,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // 12288).  The coefficients are this project's own fit: minimax in g
 // (reweighted least squares on Chebyshev nodes, |error| 1.3e-7 in ln Phi),
 // rounded to fp32.
-// Beyond 5.5 it clamps z: for x > 5.5 that is right to the last bit (with
-// TIES, for inputs that are bf16 and so often E4M3 ties themselves, the last
-// step rounds toward zero: the exact result lies below x by less than half an
-// ulp, and rounding up to x would turn the tie the wrong way); for x < -5.5 it gives -1.05e-7 for a result between that and 0.  In a block
-// whose largest result is 0.1 or more both get the code -0 (half the smallest
-// step is 2^-10 2^-12 = 2.4e-7), so gelu_tail is needed only in a block
-// without any x above 0.3 (GELU(0.3) = 0.185).  Where there is one, it also
-// has the block's largest magnitude: negative results end at -0.17.
+// Beyond 5.5 it clamps z.  For x > 5.5 that is right to the last bit; with
+// TIES (inputs that are bf16, and so often E4M3 ties themselves) the last step
+// rounds toward zero, because the exact result lies below x by less than half
+// an ulp and rounding up to x would turn the tie the wrong way.  For x < -5.5
+// it gives -1.05e-7 for a result between that and 0: in a block whose largest
+// result is 0.1 or more both get the code -0 (half the smallest step is 2^-10
+// 2^-12 = 2.4e-7), so gelu_tail is needed only in a block without any x above
+// 0.3 (GELU(0.3) = 0.185).  Where there is one, it also has the block's
+// largest magnitude: negative results end at -0.17.
 constexpr float kGeluFast = 5.5f;
 constexpr float kGeluPos = 0.3f, kGeluPosResult = 0.18f;  // GELU(0.3) = 0.1854
 

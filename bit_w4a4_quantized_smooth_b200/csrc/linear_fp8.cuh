@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
         // B200).
         if (p.one) {
 #pragma unroll
-          for (int j = 0; j < 128; j += 2) {
-            const float2 c = *reinterpret_cast<const float2*>(bs + j);
+          for (int j = 0; j < 128; j += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(bs + j);
             add2_rn(v[j], v[j + 1], v[j], v[j + 1], c.x, c.y);
+            add2_rn(v[j + 2], v[j + 3], v[j + 2], v[j + 3], c.z, c.w);
           }
           // a row without an x above 0.3 needs more care (fp8.cuh)
           const float hi = max_n<128>(v);

@@ -106,14 +106,20 @@ StreamArg stream_arg(PyObject* o, at::Device dev) {
 }
 
 // Runs `f(stream)` with the tensors' device current and without the GIL (f
-// also allocates outputs), and turns its status into an exception.
+// also allocates outputs, which belong to the stream that writes them), and
+// turns its status into an exception.
 template <typename F>
 void run(const char* what, at::Device dev, const StreamArg& s, F&& f) {
   int status = 0;
   {
     pybind11::gil_scoped_release nogil;
-    const c10::cuda::CUDAGuard guard(dev);
-    status = f(static_cast<void*>(s.given ? s.handle : c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    if (s.given) {
+      const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(s.handle, dev.index()));
+      status = f(static_cast<void*>(s.handle));
+    } else {
+      const c10::cuda::CUDAGuard guard(dev);
+      status = f(static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev.index()).stream()));
+    }
   }
   if (status != SVDQ_OK) throw StatusError{status, what};
 }

@@ -23,8 +23,9 @@
  *  - All tensors are dense, row-major, in DEVICE memory, allocated and owned
  *    by the caller.  The library allocates no device memory.  Its host-side
  *    state is a cache of encoded TMA descriptors (a pure function of the
- *    buffers' addresses and shapes, so reuse is always valid) and the
- *    kernels' shared-memory limits set per device; on the device it keeps a
+ *    buffers' addresses and shapes, so reuse is always valid), one of chosen
+ *    work splits (a function of sizes and device) and the kernels'
+ *    shared-memory limits set per device; on the device it keeps a
  *    per-device status word (see svdq_sync_status).  All calls are safe to
  *    make from several host threads.
  *  - bf16 tensors are passed as `const void*` / `void*` (IEEE bfloat16).
@@ -246,8 +247,11 @@ svdq_status svdq_channel_absmax(const void* X, int64_t M, int64_t K, float* amax
  *    NaN and does not change its block's scale; an infinity becomes
  *    +-448 2^120.
  * Conventions as above, with these sizes: K a multiple of 16, N a multiple of
- * 8 (16 for svdq_linear_fp8_gelu), M >= 1.  No call needs a workspace, and
- * equal inputs give equal bits. */
+ * 8 (16 for svdq_linear_fp8_gelu), M >= 1.  NaN and infinity are allowed: a
+ * NaN stays in its row.  No call needs a workspace, outputs overlap inputs
+ * only where that is said, and a call repeated on equal inputs gives equal
+ * bits (the order of the sums depends on M, K and N).  The scale byte 255 is
+ * NaN. */
 typedef enum { SVDQ_BF16 = 0, SVDQ_F32 = 1 } svdq_dtype;
 
 /* Bytes of the FP8 block-128 buffers for `rows` vectors of length K:
@@ -268,8 +272,8 @@ svdq_status svdq_pack_weight_fp8(const void* W, int w_dtype, int64_t K, int64_t 
  * Activation quantiser: X, or GELU(X) with gelu = 1, to FP8 block-128.
  *   X         bf16 [M][K], row stride ldx elements (ldx >= K, a multiple of
  *             8: a column range of a wider tensor)
- *   gelu      0 or 1; GELU(x) = 0.5 x (1 + erf(x / sqrt 2)) in fp32, good to
- *             about 1e-6 relative also for negative x, not rounded to bf16
+ *   gelu      0 or 1; GELU(x) = 0.5 x (1 + erf(x / sqrt 2)) in fp32, within
+ *             2^-18 relative also for negative x, not rounded to bf16
  *             before the quantiser.  (svdq_quantize_act_gelu evaluates the
  *             same function by an approximation with 3e-7 absolute error.)
  *   x_codes   uint8 [M][K] output;   x_scales   svdq_fp8_sizes(M, K) output
@@ -287,7 +291,7 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
  *   X             bf16 [M][K], row stride ldx (ldx >= K, a multiple of 8)
  *   residual      [M][K] of residual_dtype (an svdq_dtype), or NULL
  *   gamma         bf16 [K], or NULL for ones
- *   eps           >= 0, finite
+ *   eps           >= 0, finite (with 0, a row of zeros gives NaN)
  *   residual_out  [M][K] of residual_dtype: h (NULL iff residual is); may be
  *                 `residual` itself
  *   Y             bf16 [M][K] output or NULL; may be X when ldx == K

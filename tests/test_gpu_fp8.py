@@ -2,10 +2,12 @@
 
 Tolerances, from the arithmetic of each call (u = 2^-24, half an fp32 step):
 - quantise and pack without GELU: none.  Scaling by a power of two is exact.
-- GELU: |error| <= 2^-19 |GELU(x)| for inputs in [-13, 13]: the fit of
-  log2 Phi is within 1.3e-7 in ln Phi, its fp32 evaluation (|g| <= 27, ten
-  fused steps) adds up to about 8e-7, the exponential 2 u, the last product u.
-  (In a block whose largest result is 0.1 or more, values of x < -5.5 are
+- GELU: |error| <= 2^-18 |GELU(x)| for inputs in [-13, 13].  Horner's rule for
+  g = log2 Phi(-z) at z = 5.5, where it is worst, has partial values 25.7, 4.5,
+  0.61, 0.027, ... after 0, 1, 2, 3, ... more multiplications by z: half an ulp
+  of each, times z^k, is 9.5e-7 + 1.3e-6 + 9e-7 + 4e-7 = 3.6e-6 in g, 2.5e-6
+  in ln Phi; with the fit's 1.3e-7, 2.4e-7 of the exponential and u of the
+  product 2.9e-6 < 2^-18 = 3.8e-6.  (In a block whose largest result is 0.1 or more, values of x < -5.5 are
   -1.05e-7 or nearer to 0 on both sides, below half the smallest code.)
 - norm: the sum of squares is a chain of at most 32 fused steps, then two
   five-step trees, so 42 u relative, of which the root takes half; division,
@@ -23,7 +25,7 @@ from tests import _fp8_ref as ref
 
 pytestmark = pytest.mark.gpu
 
-GELU_REL = 2.0 ** -19
+GELU_REL = 2.0 ** -18
 NORM_REL = 2.0 ** -19
 
 
