@@ -217,8 +217,26 @@ __global__ void __launch_bounds__(kS8Threads)
       }
     }
   }
-  if (p.splits > 1) cluster_sync();  // every CTA's partial is in its shared memory
-  else __syncthreads();
+  // The tensor memory goes back before the CTAs meet.  Launches of other sizes
+  // (other column counts) on another stream may share the SMs; a CTA that held
+  // its columns while it waited for a CTA of its cluster, which in turn waited
+  // for columns elsewhere, could close a circle.  Warp 1 frees them between its
+  // arrival and its wait (all before the arrival: 0.1 to 0.4 us a call).
+  tc_fence_before();
+  if (p.splits > 1) {
+    cluster_arrive();
+    if (warp >= 2) named_bar_arrive(1, 160);  // this warp has read its lanes
+    if (warp == 1) {
+      named_bar_sync(1, 160);
+      tc_fence_after();
+      tmem_dealloc(tmem, p.tmem_cols);
+    }
+    cluster_wait();  // every CTA's partial is in its shared memory
+  } else {
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+  }
   const uint32_t part_u = smem_u32(part);
   const int n = n0 + 4 * lane;
   float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -263,9 +281,6 @@ __global__ void __launch_bounds__(kS8Threads)
     if (split == 0 && !aborted) zero_tile_scales(p.y_scales, vrows, m0, n0, p.N, tid, kS8Threads);
   }
   if (p.splits > 1) cluster_sync();  // no CTA leaves while another still reads its partial
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
 }
 
 }  // namespace svdq

@@ -665,3 +665,37 @@ def test_two_threads_call_at_once():
     [t.join() for t in ts]
     assert not bad, bad[:3]
     _ok()
+
+
+def test_few_rows_products_of_several_sizes_share_the_gpu():
+    """Clusters with 64, 128 and 256 columns of tensor memory a CTA, and the
+    4-bit few-rows kernel, on four streams at once: no CTA may wait for its
+    cluster while it holds columns that another one's cluster needs."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(22)
+    K, N = 2048, 1536
+    wc, ws = svdq.pack_weight_fp8(_dev(rng.normal(size=(K, N)), torch.bfloat16))
+    X8 = [svdq.quantize_fp8(_dev(rng.normal(size=(m, K)), torch.bfloat16)) for m in (1, 40, 128)]
+    rc, rs = svdq.pack_residual(_dev(rng.normal(size=(K, N)), torch.float32))
+    X4 = _dev(rng.normal(size=(64, K)), torch.bfloat16)
+    x4, x4s, _ = svdq.quantize_act(X4, torch.ones(K, device="cuda"), None)
+    svdq.set_linear_fp8_path("small")
+    svdq.set_linear_path("small")
+    try:
+        calls = [lambda x=x: svdq.linear_fp8(*x, wc, ws) for x in X8] + [
+            lambda: svdq.linear(x4, x4s, None, rc, rs, None, None, 64, K, N)]
+        want = [c() for c in calls]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in calls]
+        for _ in range(10):
+            got = [[] for _ in calls]
+            for _ in range(10):
+                for i, st in enumerate(streams):
+                    with torch.cuda.stream(st):
+                        got[i].append(calls[i]())
+            torch.cuda.synchronize()
+            assert all(torch.equal(y, w) for g, w in zip(got, want) for y in g)
+    finally:
+        svdq.set_linear_fp8_path("auto")
+        svdq.set_linear_path("auto")
+    _ok()
