@@ -58,6 +58,12 @@ Opt maybe(PyObject* o, const char* name) {
 
 void* ptr(const Opt& t) { return t ? t->data_ptr() : nullptr; }
 
+bool truth(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw python_error();
+  return t != 0;
+}
+
 constexpr auto kCodes = at::kFloat8_e4m3fn;
 constexpr auto kScales = at::kFloat8_e8m0fnu;
 
@@ -217,7 +223,7 @@ PyObject* quantize(PyObject* const* a) {
   const at::Tensor X = tensor(a[0], "X");
   const Rows r = rows_of(X, "X");
   Fp8Out out(r.M, r.K, X.device(), a[1], a[2], "x_codes", "x_scales");
-  const int gelu = PyObject_IsTrue(a[4]);
+  const int gelu = truth(a[4]);
   run("svdq_quantize_fp8", X.device(), stream_arg(a[3], X.device()), [&](void* st) {
     out.fill();
     return svdq_quantize_fp8(X.data_ptr(), r.ld, r.M, r.K, gelu, out.c(), out.s(), st);
@@ -234,7 +240,7 @@ PyObject* rmsnorm(PyObject* const* a) {
   const double eps = PyFloat_AsDouble(a[3]);
   if (eps == -1.0 && PyErr_Occurred()) throw python_error();
   Opt residual_out = maybe(a[4], "residual_out"), Y = maybe(a[5], "Y");
-  const bool fp8_out = PyObject_IsTrue(a[8]), bf16_out = PyObject_IsTrue(a[9]);
+  const bool fp8_out = truth(a[8]), bf16_out = truth(a[9]);
   if (gamma) need(*gamma, "gamma", at::kBFloat16, at::kBFloat16, {r.K}, dev);
   if (residual) {
     need(*residual, "residual", at::kBFloat16, at::kFloat, {r.M, r.K}, dev);

@@ -699,3 +699,14 @@ def test_few_rows_products_of_several_sizes_share_the_gpu():
         svdq.set_linear_fp8_path("auto")
         svdq.set_linear_path("auto")
     _ok()
+
+
+def test_flags_without_a_truth_value_are_refused():
+    torch, svdq = _m()
+    X = torch.ones((4, 256), dtype=torch.bfloat16, device="cuda")
+    two = torch.ones(2)
+    for call in (lambda: svdq.rmsnorm(X, bf16_out=two), lambda: svdq.rmsnorm(X, fp8_out=two),
+                 lambda: svdq.quantize_fp8(X, gelu=two)):
+        with pytest.raises(RuntimeError):
+            call()
+    _ok()
