@@ -348,9 +348,12 @@ __device__ __forceinline__ void zero_tile_scales(uint8_t* scales, int rows, int6
 // tile's four blocks) of R consecutive rows: a lane holds 16 columns of each
 // row (32 bytes a row, all R rows' in flight before the first is used: 128
 // bytes a thread at R = 4), 8 lanes a block; a row's four scale
-// bytes leave as one word.  (A first version with 8 columns a lane, 4 rows and
-// single scale bytes took 43.1 us for 4608 x 12288 of 21504 columns on B200,
-// 59.4 with GELU: half the loads in flight, and 2.7 us for the byte stores.)
+// bytes leave as one word.  On B200 4608 x 12288 of 21504 columns take 23.4 us
+// (170 MB, of which the codes largely stay in L2), with GELU 41.2: there the
+// polynomial bounds it (arithmetic pipes 57 and 54 % busy, issue 67 %).  64 x
+// 15360 take 4.2 us a call, which is the host's pace.  (A first version with 8
+// columns a lane, 4 rows and single scale bytes took 43.1 us, 59.4 with GELU:
+// half the loads in flight, and 2.7 us for the byte stores.)
 // The grid's last block zeroes the padding rows' scales.
 constexpr int kQ8Threads = 128;
 
@@ -420,11 +423,12 @@ __global__ void __launch_bounds__(kQ8Threads)
 //
 // A warp takes 512 columns (16 a lane, 8 lanes a block) of one row at a time,
 // S such segments in registers (h as packed bf16 where that is its type);
-// `wpr` warps share a row.  With one warp a row nothing but shuffles stands
-// between the reduction and the outputs, and 24 loads of 16 bytes a lane are in
-// flight at S = 6.  (A first version, one CTA a row and 8 columns a thread,
-// spent 37 instructions an element, mostly on reductions: 23.5 us at 4608 x
-// 3072 on B200.)
+// `wpr` warps share a row.  On B200 4608 x 3072 take 19.3 us (99 MB: 5.1 TB/s,
+// 78 % of a copy; issue 62 %, and a row's outputs wait for all of its inputs),
+// 333 x 8208 with an fp32 residual 7.4 us, one row 2.1 us of the GPU and 4.9 a
+// call, which is the host's pace.  (A first version, one CTA a row and 8 columns
+// a thread, spent 37 instructions an element, mostly on reductions: 23.5 us at
+// 4608 x 3072.)
 //
 // Rounding.  1 / sqrt(...) is carried as a sum of two fp32 numbers, h gamma is
 // exact (two 8-bit significands; with an fp32 residual its error is carried
@@ -610,11 +614,12 @@ __global__ void __launch_bounds__(kNormMaxThreads)
 // element, once per weight.
 // A CTA takes one block of 128 rows of K and 64 channels.  A thread holds 8
 // rows x 8 channels in registers: the channels' maxima meet by shuffles and
-// then in shared memory, one per warp; every thread then encodes its values, eight codes along K a channel, and only
-// the codes (one byte an element, not four) are transposed through shared
-// memory, in 16-byte chunks permuted so that neither side has bank conflicts.
-// (A first version transposed fp32 values: 43.7 us at 3072 x 12288 bf16 on
-// B200.)
+// then in shared memory, one per warp; every thread then encodes its values,
+// eight codes along K a channel, and only the codes (one byte an element, not
+// four) are transposed through shared memory, in 16-byte chunks permuted so
+// that neither side has bank conflicts.  On B200 3072 x 12288 take 25.1 us from
+// bf16 (113 MB, 69 % of a copy's rate) and 31.7 from fp32 (189 MB, 91 %).  (A
+// first version transposed fp32 values: 43.7 us from bf16.)
 constexpr int kPw8Threads = 128;
 constexpr int kPw8N = 64;
 
