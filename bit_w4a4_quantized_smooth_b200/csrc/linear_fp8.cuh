@@ -20,9 +20,10 @@ namespace svdq {
 // A tile is 24 stages of 11.4 thousand cycles together; the change to the next
 // (its last MMAs, one 64- or 128-column read of tensor memory, one arrival)
 // adds 1.9 thousand, the epilogue's arithmetic hides under the next tile.
-// A pair computes 256 x 256 output tiles, visited M-fastest; CTA c holds 128
-// of the tile's x rows and 128 of its w rows, the even CTA issues 2-SM MMAs
-// (M = 256, N = 256, K = 32).
+// A pair computes 256 x 256 output tiles; CTA c holds 128 of the tile's x rows
+// and 128 of its w rows, the even CTA issues 2-SM MMAs (M = 256, N = 256, K =
+// 32).  The tiles are visited in groups of `group` rows of tiles, M-fastest
+// within a group, so that one operand stays in L2 (l8_group in svdq.cu).
 // Ring: 5 stages of 128 columns of K per CTA (x codes and w codes, 128 rows x
 // 128 bytes each, 128-byte swizzle; a sixth changed nothing: 125.9 against
 // 125.0 us at 4608 x 3072 x 12288).  Every fourth stage of a tile also brings
@@ -56,6 +57,8 @@ struct L8Params {
   uint8_t* y_scales;   // FP8 output: scale tiles of the output rows
   int M, K, N;
   int m_tiles, tiles;  // pair tiles: ceil(M / 256) x ceil(N / 256)
+  int group;           // rows of tiles per group of the visiting order
+  int group_tiles;     // group x ceil(N / 256)
   int one;             // 1 (see the FP8 epilogue)
   uint64_t timeout_ns;
 };
@@ -124,6 +127,14 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(smem);
   auto lead = [&](const uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
+  // first row and column of tile t < p.tiles
+  auto tile_at = [&](int t, int& m, int& n) {
+    const int g = t / p.group_tiles, in = t - g * p.group_tiles;
+    const int rows = min(p.group, p.m_tiles - g * p.group);
+    const int col = in / rows;
+    m = (g * p.group + in - col * rows) * kL8BM;
+    n = col * kL8BN;
+  };
   // bytes one CTA loads for stage `it` of a tile
   auto stage_tx = [](int it) { return kL8StageBytes + ((it & 3) == 0 ? kL8SfBytes : 0u); };
 
@@ -138,7 +149,9 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     __syncwarp();
     // While the kernel ahead finishes: the w codes of the ring's first stages into L2.
     if (pair < p.tiles) {
-      const int nb = (pair / p.m_tiles) * kL8BN + 128 * static_cast<int>(rank);
+      int m, n;
+      tile_at(pair, m, n);
+      const int nb = n + 128 * static_cast<int>(rank);
       for (int it = 0; it < min(total, kL8Stages); ++it) e_tma_prefetch_2d(&tm_w, it * kL8BK, nb);
     }
     const uint32_t lead_full = lead(full);
@@ -148,8 +161,9 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     uint32_t g = 0, s = 0, ph = 1;
     bool ok = true;
     for (int t = pair; t < p.tiles && ok && !warp_flag(abort_flag); t += pairs) {
-      const int band = (t % p.m_tiles) * 2 + static_cast<int>(rank);  // this CTA's 128 rows
-      const int n0 = (t / p.m_tiles) * kL8BN;
+      int m, n0;
+      tile_at(t, m, n0);
+      const int band = (m >> 7) + static_cast<int>(rank);  // this CTA's 128 rows
       const int nb = n0 + 128 * static_cast<int>(rank);
       const int x_st = band * band_tiles, w_st = (n0 >> 7) * band_tiles;
       for (int it = 0; it < total; ++it) {
@@ -259,16 +273,19 @@ __global__ void __launch_bounds__(FP8_OUT ? kL8ThreadsFp8 : kL8Threads, 1)
     // bias columns of this thread: c0 (and c0 + 128 with one warpgroup)
     const int c0 = 128 * wg + ((tid - 64) & 127);
     auto bias_of = [&](int t, int c) {
-      const int n = (t / p.m_tiles) * kL8BN + c;
-      return (p.bias && t < p.tiles && n < N) ? __bfloat162float(p.bias[n]) : 0.0f;
+      if (!p.bias || t >= p.tiles) return 0.0f;
+      int m, n;
+      tile_at(t, m, n);
+      return n + c < N ? __bfloat162float(p.bias[n + c]) : 0.0f;
     };
     bias_s[c0] = bias_of(pair, c0);
     if constexpr (!FP8_OUT) bias_s[c0 + 128] = bias_of(pair, c0 + 128);
     int i = 0;
     for (int t = pair; t < p.tiles; t += pairs, ++i) {
       const int b = i & 1;
-      const int m0 = ((t % p.m_tiles) * 2 + static_cast<int>(rank)) * 128;
-      const int n0 = (t / p.m_tiles) * kL8BN;
+      int m0, n0;
+      tile_at(t, m0, n0);
+      m0 += 128 * static_cast<int>(rank);
       named_bar_sync(1 + wg, 128);  // this tile's bias is there, the one before is done with
       const float* bias_t = bias_s + kL8BN * b;
       const float next0 = bias_of(t + pairs, c0);

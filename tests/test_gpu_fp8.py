@@ -710,3 +710,32 @@ def test_flags_without_a_truth_value_are_refused():
         with pytest.raises(RuntimeError):
             call()
     _ok()
+
+
+@pytest.mark.parametrize("M,K,N", [(3700, 12288, 528), (1300, 32768, 1536), (300, 262144, 272)])
+def test_linear_visits_tiles_in_groups(M, K, N):
+    """x too large for L2: the tiles are visited in groups of rows of tiles
+    (2, 4 and 1 here), the last group smaller or equal."""
+    torch, svdq = _m()
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = svdq.quantize_fp8((rand(M, K) * torch.exp(rand(M, 1))).bfloat16())
+    w = svdq.pack_weight_fp8((rand(K, N) / K ** 0.5).bfloat16())
+    b = rand(N).bfloat16()
+    svdq.set_linear_fp8_path("large")
+    try:
+        Y = svdq.linear_fp8(*x, *w, b)
+        codes, scales = svdq.linear_fp8_gelu(*x, *w, b)
+    finally:
+        svdq.set_linear_fp8_path("auto")
+    _ok()
+    rows = np.unique(np.concatenate([np.arange(0, M, 41), np.arange(255, M, 256), np.arange(0, M, 256), [M - 1]]))
+    xv = torch.from_numpy(ref.decode(_np(x[0])[rows], ref.untile(_np(x[1]), M, K)[0][rows])).cuda()
+    wv = torch.from_numpy(ref.decode(_np(w[0]), ref.untile(_np(w[1]), N, K)[0])).cuda()
+    y = (xv @ wv.T + b.double()).cpu().numpy()
+    acc = (-(-K // 32) + 1) * 2.0 ** -23 * (xv.abs() @ wv.abs().T + b.double().abs()).cpu().numpy()
+    _check_y(Y[torch.from_numpy(rows).cuda()], y, acc)
+    g = ref.gelu(y)
+    s, rest = ref.untile(_np(scales), M, N)
+    assert not _np(scales)[rest].any()
+    ref.assert_encodes(_np(codes)[rows], ref.tiles(s[rows]), g, 1.13 * acc + np.abs(g) * GELU_REL)
