@@ -199,6 +199,9 @@ __global__ void __launch_bounds__(kS8Threads)
 
   // --------------------------------------------------------- epilogue --
   griddep_wait();   // the bias and Y may belong to the kernel ahead
+  const int n = n0 + 4 * lane;
+  uint2 bw = make_uint2(0, 0);  // this lane's four channels, long before they are needed
+  if (p.bias && n < p.N) bw = *reinterpret_cast<const uint2*>(p.bias + n);  // N is a multiple of 8
   __syncthreads();  // every role is done: the ring is idle, the MMAs complete
   const bool aborted = *abort_flag != 0;
   float* part = reinterpret_cast<float*>(ring);  // [bm][128], over the idle ring
@@ -242,15 +245,9 @@ __global__ void __launch_bounds__(kS8Threads)
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
   }
   const uint32_t part_u = smem_u32(part);
-  const int n = n0 + 4 * lane;
-  float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.bias && n < p.N) {  // N is a multiple of 8
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = __bfloat162float(p.bias[n + e]);
-  }
   // one token of the tile: its 128 channels, four a lane
   auto store = [&](int r, const float4& acc) {
-    float v[4] = {acc.x + b[0], acc.y + b[1], acc.z + b[2], acc.w + b[3]};
+    float v[4] = {acc.x + bf16_lo(bw.x), acc.y + bf16_hi(bw.x), acc.z + bf16_lo(bw.y), acc.w + bf16_hi(bw.y)};
     const int64_t m = m0 + r;
     if constexpr (FP8_OUT) {
       if (!aborted) store_gelu_fp8(v, static_cast<uint8_t*>(p.Y), p.y_scales, m, n, p.N, lane);
