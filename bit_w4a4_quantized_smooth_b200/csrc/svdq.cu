@@ -404,7 +404,7 @@ int s8_active(int splits, size_t smem, int sms) {
 //   + 2.0 (waves - 1)          clusters that do not fit at once
 // Against the best of all measured, its choice (of the kernel as well) costs
 // 0.5 % on average and 8 % at the worst.  The deeper ring on ties.
-svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+svdq_status s8_plan(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
   const double x = bm / 128.0;
@@ -414,7 +414,6 @@ svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t
   const uint32_t tmem_cols = pow2_at_least(static_cast<uint32_t>(bm + 32));
   const void* model = reinterpret_cast<const void*>(svdq::linear_fp8_splitk_occupancy_kernel);
   if (svdq_status rc = ensure_smem(model, dev, svdq::kS8SmemLimit)) return rc;
-  if (svdq_status rc = ensure_smem(kern, dev, svdq::kS8SmemLimit)) return rc;
   for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
     const int spc = (k_stages + s - 1) / s;
     if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
@@ -441,7 +440,7 @@ svdq_status s8_plan(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t
 // The plan is a pure function of the sizes and the device, so chosen ones are
 // kept (the occupancy calls take tens of microseconds).
 struct S8Key {
-  uint64_t words[4];
+  uint64_t words[3];
   bool operator==(const S8Key& o) const { return std::memcmp(words, o.words, sizeof(words)) == 0; }
 };
 struct S8KeyHash {
@@ -454,12 +453,11 @@ struct S8KeyHash {
 std::mutex g_s8_mu;
 std::unordered_map<S8Key, S8Plan, S8KeyHash> g_s8_plans;
 
-svdq_status s8_plan_kept(S8Plan* out, const void* kern, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+svdq_status s8_plan_kept(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   // M only through its tile count and padded tile
   const uint64_t m_class = M >= svdq::kS8MaxBM ? static_cast<uint64_t>((M + 127) / 128) << 8
                                                : static_cast<uint64_t>((M + 15) / 16);
-  const S8Key key = {{m_class | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N),
-                      static_cast<uint64_t>(reinterpret_cast<uintptr_t>(kern))}};
+  const S8Key key = {{m_class | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N)}};
   {
     std::lock_guard<std::mutex> lock(g_s8_mu);
     auto it = g_s8_plans.find(key);
@@ -468,7 +466,7 @@ svdq_status s8_plan_kept(S8Plan* out, const void* kern, int64_t M, int64_t K, in
       return SVDQ_OK;
     }
   }
-  if (svdq_status rc = s8_plan(out, kern, M, K, N, dev, sms)) return rc;
+  if (svdq_status rc = s8_plan(out, M, K, N, dev, sms)) return rc;
   std::lock_guard<std::mutex> lock(g_s8_mu);
   if (g_s8_plans.size() >= kMapCacheCap) g_s8_plans.clear();
   g_s8_plans.emplace(key, *out);
@@ -476,13 +474,15 @@ svdq_status s8_plan_kept(S8Plan* out, const void* kern, int64_t M, int64_t K, in
 }
 
 template <bool FP8_OUT>
-svdq_status launch_s8(const S8Plan& pl, const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+svdq_status launch_s8(const S8Plan& pl, int dev, const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                       const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
                       uint8_t* y_scales, void* stream) {
   CUtensorMap tm_x, tm_w;
   if (svdq_status rc = fp8_codes_map(&tm_x, x_codes, M, K, static_cast<uint32_t>(pl.bm))) return rc;
   if (svdq_status rc = fp8_codes_map(&tm_w, w_codes, N, K, svdq::kS8BN)) return rc;
-  auto kern = svdq::linear_fp8_splitk_kernel<FP8_OUT>;
+  const bool many = pl.bm > 64 && pl.splits >= 2 && pl.splits <= 4;
+  auto kern = many ? svdq::linear_fp8_splitk_kernel<FP8_OUT, true> : svdq::linear_fp8_splitk_kernel<FP8_OUT, false>;
+  if (svdq_status rc = ensure_smem(reinterpret_cast<const void*>(kern), dev, svdq::kS8SmemLimit)) return rc;
   svdq::S8Params p;
   p.x_scales = x_scales;
   p.w_scales = w_scales;
@@ -555,14 +555,12 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
   const int path = g_linear8_path.load(std::memory_order_relaxed);
   if (path == 2 || (path == 0 && M <= 2048)) {
-    const void* kern = fp8_out ? reinterpret_cast<const void*>(svdq::linear_fp8_splitk_kernel<true>)
-                               : reinterpret_cast<const void*>(svdq::linear_fp8_splitk_kernel<false>);
     S8Plan pl;
-    if (svdq_status rc = s8_plan_kept(&pl, kern, M, K, N, dev, sms)) return rc;
+    if (svdq_status rc = s8_plan_kept(&pl, M, K, N, dev, sms)) return rc;
     const double stages = static_cast<double>((K + svdq::kL8BK - 1) / svdq::kL8BK);
     if (path == 2 || pl.us < 4.5 + static_cast<double>(pair_waves) * (0.30 * stages + 0.75))
-      return fp8_out ? launch_s8<true>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, stream)
-                     : launch_s8<false>(pl, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, stream);
+      return fp8_out ? launch_s8<true>(pl, dev, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, stream)
+                     : launch_s8<false>(pl, dev, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, stream);
   }
 
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws, tm_y;
