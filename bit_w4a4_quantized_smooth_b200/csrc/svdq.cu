@@ -402,9 +402,13 @@ int s8_active(int splits, size_t smem, int sms) {
 //                              a stage: its issue; the latency of a load over
 //                              the ring's depth; the SM's share of its loads
 //   + 2.0 (waves - 1)          clusters that do not fit at once
+//   + 0.25 passes              with GELU: six warps take a token each at a time
 // Against the best of all measured, its choice (of the kernel as well) costs
-// 0.5 % on average and 8 % at the worst.  The deeper ring on ties.
-svdq_status s8_plan(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+// 0.5 % on average and 8 % at the worst; with GELU, at 112 sizes of M 1 to 1024
+// and against this choice without the last term and the large-M kernel, 1 % on
+// average and 22 % at the worst (512 x 12288 x 3072), where that choice lost 8
+// and 62 %.  The deeper ring on ties.
+svdq_status s8_plan(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
   const double x = bm / 128.0;
@@ -416,6 +420,7 @@ svdq_status s8_plan(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int s
   if (svdq_status rc = ensure_smem(model, dev, svdq::kS8SmemLimit)) return rc;
   for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
     const int spc = (k_stages + s - 1) / s;
+    const int passes = ((bm + s - 1) / s + 5) / 6;
     if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
     for (int depth = std::min(spc, 3); depth <= std::min(spc, 8); ++depth) {
       const uint32_t ring = std::max<uint32_t>(depth * stage, static_cast<uint32_t>(bm) * svdq::kS8BN * 4);
@@ -428,7 +433,7 @@ svdq_status s8_plan(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int s
       const double occ = std::max(1.0, std::min<double>(ctas, active) / sms);
       const double per = std::max({0.21, 0.71 * (1.0 + 1.3 * x) / depth, (0.097 + 0.13 * x) * occ});
       const double us = 2.0 + 0.97 * x + (s > 1 ? 1.9 : 0.0) + 0.0037 * ctas + waves * spc * per + 2.0 * (waves - 1) -
-                        0.02 * depth;
+                        0.02 * depth + (gelu ? 0.25 * passes : 0.0);
       if (best.splits == 0 || us < best.us) best = {bm, s, spc, depth, tmem_cols, smem, us};
     }
   }
@@ -453,11 +458,11 @@ struct S8KeyHash {
 std::mutex g_s8_mu;
 std::unordered_map<S8Key, S8Plan, S8KeyHash> g_s8_plans;
 
-svdq_status s8_plan_kept(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+svdq_status s8_plan_kept(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   // M only through its tile count and padded tile
   const uint64_t m_class = M >= svdq::kS8MaxBM ? static_cast<uint64_t>((M + 127) / 128) << 8
                                                : static_cast<uint64_t>((M + 15) / 16);
-  const S8Key key = {{m_class | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N)}};
+  const S8Key key = {{m_class | static_cast<uint64_t>(gelu) << 47 | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N)}};
   {
     std::lock_guard<std::mutex> lock(g_s8_mu);
     auto it = g_s8_plans.find(key);
@@ -466,7 +471,7 @@ svdq_status s8_plan_kept(S8Plan* out, int64_t M, int64_t K, int64_t N, int dev, 
       return SVDQ_OK;
     }
   }
-  if (svdq_status rc = s8_plan(out, M, K, N, dev, sms)) return rc;
+  if (svdq_status rc = s8_plan(out, gelu, M, K, N, dev, sms)) return rc;
   std::lock_guard<std::mutex> lock(g_s8_mu);
   if (g_s8_plans.size() >= kMapCacheCap) g_s8_plans.clear();
   g_s8_plans.emplace(key, *out);
@@ -547,7 +552,7 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   const int sms = sm_count(dev);
   if (sms < 2) return SVDQ_ERR_CUDA;
   // The few-rows kernel where its estimate is below the large-M kernel's, 4.5
-  // us + (0.30 a stage of 128 columns + 0.75) for every wave of CTA pairs
+  // us (6.1 with GELU) + (0.30 a stage of 128 columns + 0.75) for every wave of CTA pairs
   // (measured on B200: 12.2 us against 8.0 at 128 x 3072 x 3072, 33.6 against
   // 17.6 at 256 x 12288 x 3072 and 28.0 at 512, but 14.2 against 15.8 at 256 x
   // 3072 x 12288 and 14.4 against 14.9 at 512 x 3072 x 9216).
@@ -556,9 +561,9 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   const int path = g_linear8_path.load(std::memory_order_relaxed);
   if (path == 2 || (path == 0 && M <= 2048)) {
     S8Plan pl;
-    if (svdq_status rc = s8_plan_kept(&pl, M, K, N, dev, sms)) return rc;
+    if (svdq_status rc = s8_plan_kept(&pl, fp8_out, M, K, N, dev, sms)) return rc;
     const double stages = static_cast<double>((K + svdq::kL8BK - 1) / svdq::kL8BK);
-    if (path == 2 || pl.us < 4.5 + static_cast<double>(pair_waves) * (0.30 * stages + 0.75))
+    if (path == 2 || pl.us < (fp8_out ? 6.1 : 4.5) + static_cast<double>(pair_waves) * (0.30 * stages + 0.75))
       return fp8_out ? launch_s8<true>(pl, dev, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, y_scales, stream)
                      : launch_s8<false>(pl, dev, x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, stream);
   }
