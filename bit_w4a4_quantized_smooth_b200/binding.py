@@ -260,9 +260,9 @@ def channel_absmax(X, amax=None, stream=None):
 # the same sizes are taken as well).  Types, shapes, strides and devices are
 # checked (ValueError) in the native module _svdq_torch (csrc/torch_calls.cpp),
 # which allocates the outputs that are not given (on the stream that writes
-# them; codes and scales share an allocation) and makes the C ABI's call on the
-# device of the first argument, on that device's current stream unless one is
-# given.  Forward only: no gradients are recorded.
+# them; codes and scales share an allocation, as do all outputs of a call that
+# need 1 MiB or less) and makes the C ABI's call on the device of the first
+# argument, on that device's current stream unless one is given.  Forward only: no gradients are recorded.
 
 _ext = None
 

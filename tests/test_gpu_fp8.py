@@ -739,3 +739,26 @@ def test_linear_visits_tiles_in_groups(M, K, N):
     s, rest = ref.untile(_np(scales), M, N)
     assert not _np(scales)[rest].any()
     ref.assert_encodes(_np(codes)[rows], ref.tiles(s[rows]), g, 1.13 * acc + np.abs(g) * GELU_REL)
+
+
+@pytest.mark.parametrize("M", [1, 77, 700])
+def test_outputs_made_by_a_call_are_apart(M):
+    """Small outputs share an allocation: 256-byte aligned parts that do not
+    overlap.  A large residual or bf16 output holds no other one's memory."""
+    torch, svdq = _m()
+    K = 1040
+    X, R = (torch.randn((M, K), device="cuda").bfloat16() for _ in range(2))
+    outs = svdq.rmsnorm(X, None, R.float(), bf16_out=True)
+    want = svdq.rmsnorm(X, None, R.float(), residual_out=torch.empty((M, K), device="cuda"), Y=torch.empty_like(X),
+                        x_codes=torch.empty((M, K), dtype=torch.float8_e4m3fn, device="cuda"),
+                        x_scales=torch.zeros(svdq.fp8_sizes(M, K)[1], dtype=torch.uint8, device="cuda"))
+    _ok()
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in outs)
+    assert all(a % 256 == 0 for a, _ in spans)
+    assert all(e <= b for (_, e), (b, _) in zip(spans, spans[1:]))
+    for t, w in zip(outs, want):
+        assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+        assert t.is_contiguous() and t.untyped_storage().nbytes() >= t.numel() * t.element_size()
+    if M == 700:
+        for t in outs[2:]:
+            assert t.untyped_storage().nbytes() < t.numel() * t.element_size() + 256
