@@ -12,9 +12,9 @@
 // splits, ... of every CTA's partial in rank order, adds the bias and stores
 // (bf16, or GELU and the FP8 block of the token's 128 channels, which is
 // exactly one warp's row).  No global scratch, and the sum's order is fixed.
-// On B200, weights from HBM: 1 x 3072 x 9216 takes 8.0 us (28.3 MB, 3.5 TB/s),
-// 1 x 3072 x 3072 5.2, 16 x 3072 x 12288 with GELU 9.7, 128 x 3072 x 3072 8.1.
-// About 4 us of each are launch, first loads, exchange and stores, during which
+// On B200, weights from HBM: 1 x 3072 x 9216 takes 7.5 us (28.3 MB, 3.8 TB/s),
+// 1 x 3072 x 3072 4.7, 16 x 3072 x 12288 with GELU 9.2, 128 x 3072 x 3072 7.7.
+// About 3 us of each are launch, first loads, exchange and stores, during which
 // the weights do not stream; a plain kernel that only loads 37.7 MB takes 8.5.
 #pragma once
 

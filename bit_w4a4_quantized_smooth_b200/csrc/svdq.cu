@@ -553,9 +553,9 @@ svdq_status linear_fp8_impl(const uint8_t* x_codes, const uint8_t* x_scales, con
   if (sms < 2) return SVDQ_ERR_CUDA;
   // The few-rows kernel where its estimate is below the large-M kernel's, 4.5
   // us (6.1 with GELU) + (0.30 a stage of 128 columns + 0.75) for every wave of CTA pairs
-  // (measured on B200: 12.2 us against 8.0 at 128 x 3072 x 3072, 33.6 against
-  // 17.6 at 256 x 12288 x 3072 and 28.0 at 512, but 14.2 against 15.8 at 256 x
-  // 3072 x 12288 and 14.4 against 14.9 at 512 x 3072 x 9216).
+  // (measured on B200: 12.0 us against 7.8 at 128 x 3072 x 3072, 33.5 against
+  // 17.3 at 256 x 12288 x 3072 and 29.4 at 512, but 14.3 against 15.3 at 256 x
+  // 3072 x 12288 and 14.1 against 15.5 at 512 x 3072 x 9216).
   const int64_t pair_tiles = ((M + svdq::kL8BM - 1) / svdq::kL8BM) * ((N + svdq::kL8BN - 1) / svdq::kL8BN);
   const int64_t pair_waves = (pair_tiles + sms / 2 - 1) / (sms / 2);
   const int path = g_linear8_path.load(std::memory_order_relaxed);
