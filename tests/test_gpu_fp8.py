@@ -762,3 +762,33 @@ def test_outputs_made_by_a_call_are_apart(M):
     if M == 700:
         for t in outs[2:]:
             assert t.untyped_storage().nbytes() < t.numel() * t.element_size() + 256
+
+
+@pytest.mark.parametrize("M,K,N", [(96, 3072, 9208), (77, 2064, 5000), (70, 2576, 6152), (129, 1552, 5128),
+                                   (256, 3072, 3080), (127, 1040, 9600), (200, 4112, 2568)])
+def test_linear_few_rows_with_many_tokens(M, K, N):
+    """Two to four CTAs share a tile of more than 64 tokens (several tokens'
+    partials are added at a time), and their neighbours."""
+    torch, svdq = _m()
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = svdq.quantize_fp8((rand(M, K) * torch.exp(rand(M, 1))).bfloat16())
+    svdq.set_linear_fp8_path("small")
+    try:
+        for n in (N, N // 16 * 16):
+            w = svdq.pack_weight_fp8((rand(K, n) / K ** 0.5).bfloat16())
+            b = rand(n).bfloat16()
+            gelu = n != N or N % 16 == 0
+            out = svdq.linear_fp8_gelu(*x, *w, b) if gelu else svdq.linear_fp8(*x, *w, b)
+            _ok()
+            xv = torch.from_numpy(ref.decode(_np(x[0]), ref.untile(_np(x[1]), M, K)[0])).cuda()
+            wv = torch.from_numpy(ref.decode(_np(w[0]), ref.untile(_np(w[1]), n, K)[0])).cuda()
+            y = (xv @ wv.T + b.double()).cpu().numpy()
+            acc = (-(-K // 32) + 1) * 2.0 ** -23 * (xv.abs() @ wv.abs().T + b.double().abs()).cpu().numpy()
+            if gelu:
+                g = ref.gelu(y)
+                ref.assert_encodes(_np(out[0]), _np(out[1]), g, 1.13 * acc + np.abs(g) * GELU_REL)
+            else:
+                _check_y(out, y, acc)
+    finally:
+        svdq.set_linear_fp8_path("auto")
