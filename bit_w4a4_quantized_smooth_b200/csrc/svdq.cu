@@ -401,13 +401,14 @@ int s8_active(int splits, size_t smem, int sms) {
 //   + waves spc max(0.21, 0.71 (1 + 1.3 x) / depth, (0.097 + 0.13 x) occ)
 //                              a stage: its issue; the latency of a load over
 //                              the ring's depth; the SM's share of its loads
-//   + 2.0 (waves - 1)          clusters that do not fit at once
+//   + 6.0 (waves - 1)          clusters that do not fit at once
 //   + 0.25 passes              with GELU: six warps take a token each at a time
 // Against the best of all measured, its choice (of the kernel as well) costs
-// 0.5 % on average and 8 % at the worst; with GELU, at 112 sizes of M 1 to 1024
-// and against this choice without the last term and the large-M kernel, 1 % on
-// average and 22 % at the worst (512 x 12288 x 3072), where that choice lost 8
-// and 62 %.  The deeper ring on ties.
+// 0.5 % on average and 8 % at the worst.  At 110 other sizes (M 1 to 1024),
+// against this choice with 2 and 4 us a wave and the large-M kernel: 0.3 % on
+// average, 2 % at the worst for bf16 and 6 % with GELU (2 us a wave lost 41 %
+// at 512 x 12288 x 3072; a choice that does not count the GELU 8 % on average
+// and 62 % at the worst).  The deeper ring on ties.
 svdq_status s8_plan(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
@@ -432,7 +433,7 @@ svdq_status s8_plan(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int
       const double waves = std::ceil(ctas / active);
       const double occ = std::max(1.0, std::min<double>(ctas, active) / sms);
       const double per = std::max({0.21, 0.71 * (1.0 + 1.3 * x) / depth, (0.097 + 0.13 * x) * occ});
-      const double us = 2.0 + 0.97 * x + (s > 1 ? 1.9 : 0.0) + 0.0037 * ctas + waves * spc * per + 2.0 * (waves - 1) -
+      const double us = 2.0 + 0.97 * x + (s > 1 ? 1.9 : 0.0) + 0.0037 * ctas + waves * spc * per + 6.0 * (waves - 1) -
                         0.02 * depth + (gelu ? 0.25 * passes : 0.0);
       if (best.splits == 0 || us < best.us) best = {bm, s, spc, depth, tmem_cols, smem, us};
     }
