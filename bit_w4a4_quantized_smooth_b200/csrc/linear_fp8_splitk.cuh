@@ -12,8 +12,8 @@
 // splits, ... of every CTA's partial in rank order, adds the bias and stores
 // (bf16, or GELU and the FP8 block of the token's 128 channels, which is
 // exactly one warp's row).  No global scratch, and the sum's order is fixed.
-// On B200, weights from HBM: 1 x 3072 x 9216 takes 7.5 us (28.3 MB, 3.8 TB/s),
-// 1 x 3072 x 3072 4.7, 16 x 3072 x 12288 with GELU 9.2, 128 x 3072 x 3072 7.7.
+// On B200, weights from HBM: 1 x 3072 x 9216 takes 7.4 us (28.3 MB, 3.8 TB/s),
+// 1 x 3072 x 3072 4.4, 16 x 3072 x 12288 with GELU 9.1, 128 x 3072 x 3072 7.8.
 // About 3 us of each are launch, first loads, exchange and stores, during which
 // the weights do not stream; a plain kernel that only loads 37.7 MB takes 8.5.
 #pragma once
@@ -212,11 +212,14 @@ __global__ void __launch_bounds__(kS8Threads)
   const int n = n0 + 4 * lane;
   uint2 bw = make_uint2(0, 0);  // this lane's four channels, long before they are needed
   if (p.bias && n < p.N) bw = *reinterpret_cast<const uint2*>(p.bias + n);  // N is a multiple of 8
-  __syncthreads();  // every role is done: the ring is idle, the MMAs complete
-  const bool aborted = *abort_flag != 0;
-  float* part = reinterpret_cast<float*>(ring);  // [bm][128], over the idle ring
-  const int vrows = min(p.bm, p.M - m0);         // tokens of this tile
-  if (warp >= 2 && !aborted && warp_wait(smem_u32(fin), 0, p.timeout_ns, 84)) {
+  // [bm][128], over the ring: once the MMAs are complete every stage that was
+  // loaded has been read.  (After an abort a copy may still land in it; the sums
+  // are not stored then.)
+  float* part = reinterpret_cast<float*>(ring);
+  const int vrows = min(p.bm, p.M - m0);  // tokens of this tile
+  if (warp >= 2 && !warp_wait(smem_u32(fin), 0, p.timeout_ns, 84)) {
+    *abort_flag = 1;
+  } else if (warp >= 2) {
     tc_fence_after();
     const int q = warp & 3;
     const uint32_t src = tmem + (static_cast<uint32_t>(32 * q) << 16);
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kS8Threads)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
   }
+  const bool aborted = *abort_flag != 0;
   const uint32_t part_u = smem_u32(part);
   // one token of the tile: its 128 channels, four a lane
   auto store = [&](int r, const float4& acc) {
