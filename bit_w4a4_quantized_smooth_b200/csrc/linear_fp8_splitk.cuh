@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kS8Threads)
           make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   };
-  if (p.splits == 1) {
+  if (!MANY && p.splits == 1) {
 #pragma unroll 4
     for (int r = warp; r < vrows; r += kS8Threads / 32)
       store(r, *reinterpret_cast<const float4*>(part + r * kS8BN + 4 * lane));
