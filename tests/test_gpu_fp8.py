@@ -792,3 +792,31 @@ def test_linear_few_rows_with_many_tokens(M, K, N):
                 _check_y(out, y, acc)
     finally:
         svdq.set_linear_fp8_path("auto")
+
+
+@pytest.mark.parametrize("N", [8, 72, 136, 192, 256 + 72])
+@pytest.mark.parametrize("K", [16, 640])
+def test_linear_tiles_that_end_inside_n(N, K):
+    """Tiles of which only the first 64 to 192 columns are stored, several for
+    each CTA pair, so both accumulators meet them: a group of columns without a
+    store must not let the next one overwrite what a store still reads."""
+    torch, svdq = _m()
+    M = 60000 + 40                                             # 235 rows of tiles for 74 pairs; the last warp rows clipped
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = svdq.quantize_fp8((rand(M, K) * torch.exp(rand(M, 1))).bfloat16())
+    w = svdq.pack_weight_fp8((rand(K, N) / K ** 0.5).bfloat16())
+    b = rand(N).bfloat16()
+    svdq.set_linear_fp8_path("large")
+    try:
+        Y = svdq.linear_fp8(*x, *w, b)
+        for _ in range(20):
+            assert torch.equal(Y, svdq.linear_fp8(*x, *w, b))
+    finally:
+        svdq.set_linear_fp8_path("auto")
+    _ok()
+    xv = torch.from_numpy(ref.decode(_np(x[0]), ref.untile(_np(x[1]), M, K)[0])).cuda()
+    wv = torch.from_numpy(ref.decode(_np(w[0]), ref.untile(_np(w[1]), N, K)[0])).cuda()
+    y = (xv @ wv.T + b.double()).cpu().numpy()
+    acc = (-(-K // 32) + 1) * 2.0 ** -23 * (xv.abs() @ wv.abs().T + b.double().abs()).cpu().numpy()
+    _check_y(Y, y, acc)
