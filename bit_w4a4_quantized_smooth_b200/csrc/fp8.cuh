@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(kQ8Threads)
 // turn half of those the wrong way.
 constexpr int kNormMaxThreads = 512;
 
-// 1 / sqrt(sum / K + eps) as hi + lo.
+// 1 / sqrt(sum / K + eps) as hi + lo.  lo is 0 where hi^2 leaves fp32's range:
+// below 2.9e-39 (s has 22 bits or fewer there), at zero and at infinity.
 __device__ __forceinline__ void norm_rstd(float sum, float K, float eps, float& hi, float& lo) {
   const float q = __fdiv_rn(sum, K);
   const float q_lo = __fmaf_rn(-q, K, sum) * rcp_approx(K);
@@ -451,7 +452,7 @@ __device__ __forceinline__ void norm_rstd(float sum, float K, float eps, float& 
   float e = __fmaf_rn(-s, p, 1.0f);
   e = __fmaf_rn(-s, __fmaf_rn(hi, hi, -p), e);
   e = __fmaf_rn(-s_lo, p, e);
-  lo = s > 0.0f && s <= 3.402823466e38f ? __fmul_rn(__fmul_rn(0.5f, hi), e) : 0.0f;
+  lo = p > 0.0f && p <= 3.402823466e38f ? __fmul_rn(__fmul_rn(0.5f, hi), e) : 0.0f;
 }
 
 template <int S, typename RES>

@@ -287,11 +287,16 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
  *     y = h / sqrt(mean_k(h^2) + eps) * gamma,
  * y to FP8 block-128 and / or bf16.  The norm is taken of the stored h, so the
  * result is that of an addition and a norm of their own; sums, root and
- * products are fp32, each output rounded once.
+ * products are fp32, each output rounded once.  The squares are fp32 numbers
+ * too: a row whose root mean square is below 2^-64 (5e-20) loses precision
+ * unless eps is above it (y is off by 2^-149 / (mean + eps) relative), one
+ * whose squares are all below 2^-150 counts as a row of zeros, and one whose
+ * sum of squares exceeds 2^128 gives zeros.
  *   X             bf16 [M][K], row stride ldx (ldx >= K, a multiple of 8)
  *   residual      [M][K] of residual_dtype (an svdq_dtype), or NULL
  *   gamma         bf16 [K], or NULL for ones
- *   eps           >= 0, finite (with 0, a row of zeros gives NaN)
+ *   eps           >= 0, finite (with 0, a row of zeros gives NaN, and one that
+ *                 counts as such infinities or NaN)
  *   residual_out  [M][K] of residual_dtype: h (NULL iff residual is); may be
  *                 `residual` itself
  *   Y             bf16 [M][K] output or NULL; may be X when ldx == K

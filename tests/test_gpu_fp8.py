@@ -820,3 +820,27 @@ def test_linear_tiles_that_end_inside_n(N, K):
     y = (xv @ wv.T + b.double()).cpu().numpy()
     acc = (-(-K // 32) + 1) * 2.0 ** -23 * (xv.abs() @ wv.abs().T + b.double().abs()).cpu().numpy()
     _check_y(Y, y, acc)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-39, 1e-30])
+def test_rmsnorm_of_rows_near_the_bottom_of_fp32(eps):
+    """Rows whose mean square is a subnormal fp32 number, with an eps of that
+    size or none.  There every square, the mean, eps and their sum are off by
+    half a subnormal step, 2^-150, each: 4 of them, and the root takes half."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(17)
+    h = rng.normal(size=(6, 400)) * np.array([3e-21, 1e-20, 3e-20, 6e-20, 1e-19, 1e-18])[:, None]
+    X = _dev(h, torch.bfloat16)
+    R = torch.zeros((6, 400), dtype=torch.float32, device="cuda")
+    G = _dev(1 + 0.1 * rng.normal(size=400), torch.bfloat16)
+    for res in (None, R):
+        codes, scales, _, Y = svdq.rmsnorm(X, G, res, eps=eps, bf16_out=True)
+        _ok()
+        x = _np(X)
+        s = (x * x).mean(axis=1, keepdims=True) + eps
+        y = x / np.sqrt(s) * _np(G)
+        err = np.abs(y) * (NORM_REL + 2.0 ** -149 / s)
+        ref.assert_encodes(_np(codes), _np(scales), y, err)
+        got, ok = _np(Y), np.abs(y) > 1e-30
+        assert (got[ok] >= ref.bf16_round(y - err)[ok]).all() and (got[ok] <= ref.bf16_round(y + err)[ok]).all()
+        assert np.abs(got[~ok]).max(initial=0.0) <= 1.01e-30
