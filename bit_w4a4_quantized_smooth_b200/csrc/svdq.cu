@@ -209,7 +209,33 @@ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) ==
 
 bool valid_rank(int64_t r) { return r >= 0 && r <= 128 && r % 16 == 0; }
 
-svdq_status launch_status() { return cudaGetLastError() == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA; }
+// Every entry that reaches the CUDA runtime runs in here.  A launch is judged
+// by its own return value, not by cudaGetLastError(), which may hold an error
+// of the caller's; a call that fails takes its own error off that slot again,
+// where the next check of the program (torch shares the runtime) would find it.
+// The caches of maps, plans and limits allocate: no exception leaves a C call.
+template <typename F>
+svdq_status guarded(F&& f) {
+  svdq_status rc = SVDQ_ERR_CUDA;
+  try {
+    rc = f();
+  } catch (...) {
+  }
+  if (rc == SVDQ_ERR_CUDA) cudaGetLastError();
+  return rc;
+}
+
+svdq_status launched(cudaError_t e) { return e == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA; }
+
+// A plain launch: one block shape, no dynamic shared memory, no attributes.
+template <typename... P, typename... A>
+svdq_status launch_plain(void (*kern)(P...), dim3 grid, unsigned threads, void* stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  return launched(cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...));
+}
 
 uint32_t pow2_at_least(uint32_t x) {
   uint32_t p = 32;
@@ -305,10 +331,7 @@ svdq_status launch_linear_splitk(const CUtensorMap& tm_xc, const CUtensorMap& tm
   }
   cfg.attrs = attr;
   cfg.numAttrs = add_overlap_attr(attr, na);
-  if (cudaLaunchKernelEx(&cfg, svdq::linear_splitk_kernel, tm_xc, tm_rc, tm_xs, tm_rs, tm_t, tm_l2, p) !=
-      cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  return launch_status();
+  return launched(cudaLaunchKernelEx(&cfg, svdq::linear_splitk_kernel, tm_xc, tm_rc, tm_xs, tm_rs, tm_t, tm_l2, p));
 }
 
 // ------------------------------------------------------------ 8-bit layer --
@@ -332,8 +355,7 @@ svdq_status launch(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem,
   }
   cfg.attrs = attr;
   cfg.numAttrs = add_overlap_attr(attr, na);
-  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) != cudaSuccess) return SVDQ_ERR_CUDA;
-  return launch_status();
+  return launched(cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...));
 }
 
 // Codes [rows][K] as boxes of 128 columns x `box_rows` rows, 128-byte swizzle.
@@ -371,7 +393,10 @@ int s8_active(int splits, size_t smem, int sms) {
   const void* kern = reinterpret_cast<const void*>(svdq::linear_fp8_splitk_occupancy_kernel);
   if (splits == 1) {
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, svdq::kS8Threads, smem) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, svdq::kS8Threads, smem) != cudaSuccess) {
+      cudaGetLastError();  // this split is passed over; no error of the call
+      return 0;
+    }
     return per_sm * sms;
   }
   cudaLaunchConfig_t cfg = {};
@@ -386,7 +411,10 @@ int s8_active(int splits, size_t smem, int sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
   return n * splits;
 }
 
@@ -507,16 +535,6 @@ svdq_status launch_s8(const S8Plan& pl, int dev, const uint8_t* x_codes, const u
   const dim3 grid(static_cast<unsigned>(pl.splits), static_cast<unsigned>((N + svdq::kS8BN - 1) / svdq::kS8BN),
                   static_cast<unsigned>((M + svdq::kS8MaxBM - 1) / svdq::kS8MaxBM));
   return launch(kern, grid, svdq::kS8Threads, pl.smem, static_cast<unsigned>(pl.splits), stream, tm_x, tm_w, p);
-}
-
-// The caches of maps and plans allocate: no exception leaves a C call.
-template <typename F>
-svdq_status no_throw(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return SVDQ_ERR_CUDA;
-  }
 }
 
 // Rows of 256-row tiles per group of the large-M kernel's visiting order.  The
@@ -662,21 +680,24 @@ svdq_status svdq_pack_residual(const float* R, int64_t K, int64_t N, uint8_t* r_
   if (K % 64 != 0 || N % 16 != 0 || K > kMaxK || N > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(R) || !aligned16(r_codes) || !aligned16(r_scales)) return SVDQ_ERR_MISALIGNED;
   dim3 grid(static_cast<unsigned>((N + 127) / 128), static_cast<unsigned>(K / 64));
-  svdq::pack_residual_kernel<<<grid, svdq::kPackThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      R, static_cast<int>(K), static_cast<int>(N), r_codes, r_scales);
-  return launch_status();
+  return guarded([&] {
+    return launch_plain(svdq::pack_residual_kernel, grid, svdq::kPackThreads, stream, R, static_cast<int>(K),
+                        static_cast<int>(N), r_codes, r_scales);
+  });
 }
 
 svdq_status svdq_quantize_act_workspace(int64_t M, int64_t K, int64_t r, size_t* bytes) {
   if (!bytes || M <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARG;
   if (K % 64 != 0 || !valid_rank(r) || M > kMaxRows || K > kMaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-  const int dev = current_device();
-  if (dev < 0) return SVDQ_ERR_CUDA;
-  const int sms = sm_count(dev);
-  if (sms <= 0) return SVDQ_ERR_CUDA;
-  const QaPlan pl = qa_plan(M, K, sms);
-  *bytes = svdq::qa_workspace_bytes(pl.row_tiles, pl.splits, static_cast<int>(r));
-  return SVDQ_OK;
+  return guarded([&] {
+    const int dev = current_device();
+    if (dev < 0) return SVDQ_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SVDQ_ERR_CUDA;
+    const QaPlan pl = qa_plan(M, K, sms);
+    *bytes = svdq::qa_workspace_bytes(pl.row_tiles, pl.splits, static_cast<int>(r));
+    return SVDQ_OK;
+  });
 }
 
 namespace {
@@ -688,15 +709,19 @@ svdq_status quantize_act_impl(const void* X, const float* inv_lambda, const void
 svdq_status svdq_quantize_act(const void* X, const float* inv_lambda, const void* L1, int64_t M, int64_t K,
                               int64_t r, uint8_t* x_codes, uint8_t* x_scales, void* T, void* workspace,
                               size_t workspace_bytes, void* stream) {
-  return quantize_act_impl(X, inv_lambda, L1, M, K, r, x_codes, x_scales, T, workspace, workspace_bytes, stream,
-                           false);
+  return guarded([&] {
+    return quantize_act_impl(X, inv_lambda, L1, M, K, r, x_codes, x_scales, T, workspace, workspace_bytes, stream,
+                             false);
+  });
 }
 
 svdq_status svdq_quantize_act_gelu(const void* X, const float* inv_lambda, const void* L1, int64_t M, int64_t K,
                                    int64_t r, uint8_t* x_codes, uint8_t* x_scales, void* T, void* workspace,
                                    size_t workspace_bytes, void* stream) {
-  return quantize_act_impl(X, inv_lambda, L1, M, K, r, x_codes, x_scales, T, workspace, workspace_bytes, stream,
-                           true);
+  return guarded([&] {
+    return quantize_act_impl(X, inv_lambda, L1, M, K, r, x_codes, x_scales, T, workspace, workspace_bytes, stream,
+                             true);
+  });
 }
 
 namespace {
@@ -805,9 +830,7 @@ svdq_status quantize_act_impl(const void* X, const float* inv_lambda, const void
   cudaLaunchAttribute attr[1];
   cfg.attrs = attr;
   cfg.numAttrs = add_overlap_attr(attr, 0);
-  if (cudaLaunchKernelEx(&cfg, kfn, tm_x, tm_l1, tm_xc, p) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  return launch_status();
+  return launched(cudaLaunchKernelEx(&cfg, kfn, tm_x, tm_l1, tm_xc, p));
 }
 }  // namespace
 
@@ -817,9 +840,10 @@ svdq_status svdq_linear(const uint8_t* x_codes, const uint8_t* x_scales, const v
   return svdq_linear_scaled(x_codes, x_scales, T, r_codes, r_scales, L2, bias, M, K, N, r, 1.0f, Y, stream);
 }
 
-svdq_status svdq_linear_scaled(const uint8_t* x_codes, const uint8_t* x_scales, const void* T,
-                               const uint8_t* r_codes, const uint8_t* r_scales, const void* L2, const void* bias,
-                               int64_t M, int64_t K, int64_t N, int64_t r, float alpha, void* Y, void* stream) {
+namespace {
+svdq_status linear_impl(const uint8_t* x_codes, const uint8_t* x_scales, const void* T, const uint8_t* r_codes,
+                        const uint8_t* r_scales, const void* L2, const void* bias, int64_t M, int64_t K, int64_t N,
+                        int64_t r, float alpha, void* Y, void* stream) {
   // alpha: a power of two in [2^-100, 2^100] (the product acc * alpha is then exact)
   int alpha_exp = 0;
   if (!(alpha > 0.0f) || !std::isfinite(alpha) || std::frexp(alpha, &alpha_exp) != 0.5f || alpha_exp < -99 ||
@@ -940,9 +964,16 @@ svdq_status svdq_linear_scaled(const uint8_t* x_codes, const uint8_t* x_scales, 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = add_overlap_attr(attr, 1);
-  if (cudaLaunchKernelEx(&cfg, kern, tm_xc, tm_rc, tm_xs, tm_rs, tm_t, tm_l2, tm_y, p) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  return launch_status();
+  return launched(cudaLaunchKernelEx(&cfg, kern, tm_xc, tm_rc, tm_xs, tm_rs, tm_t, tm_l2, tm_y, p));
+}
+}  // namespace
+
+svdq_status svdq_linear_scaled(const uint8_t* x_codes, const uint8_t* x_scales, const void* T,
+                               const uint8_t* r_codes, const uint8_t* r_scales, const void* L2, const void* bias,
+                               int64_t M, int64_t K, int64_t N, int64_t r, float alpha, void* Y, void* stream) {
+  return guarded([&] {
+    return linear_impl(x_codes, x_scales, T, r_codes, r_scales, L2, bias, M, K, N, r, alpha, Y, stream);
+  });
 }
 
 // ------------------------------------------------------------- 8-bit layer --
@@ -963,11 +994,13 @@ svdq_status svdq_pack_weight_fp8(const void* W, int w_dtype, int64_t K, int64_t 
   if (!aligned16(W) || !aligned16(w_codes) || !aligned16(w_scales)) return SVDQ_ERR_MISALIGNED;
   const dim3 grid(static_cast<unsigned>((N + 127) / 128 * (128 / svdq::kPw8N)),
                   static_cast<unsigned>(4 * svdq::fp8_band_tiles(K)));
-  if (w_dtype == SVDQ_BF16)
-    return launch(svdq::pack_weight_fp8_kernel<__nv_bfloat16>, grid, svdq::kPw8Threads, 0, 1, stream,
-                  static_cast<const __nv_bfloat16*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
-  return launch(svdq::pack_weight_fp8_kernel<float>, grid, svdq::kPw8Threads, 0, 1, stream,
-                static_cast<const float*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
+  return guarded([&] {
+    if (w_dtype == SVDQ_BF16)
+      return launch(svdq::pack_weight_fp8_kernel<__nv_bfloat16>, grid, svdq::kPw8Threads, 0, 1, stream,
+                    static_cast<const __nv_bfloat16*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
+    return launch(svdq::pack_weight_fp8_kernel<float>, grid, svdq::kPw8Threads, 0, 1, stream,
+                  static_cast<const float*>(W), static_cast<int>(K), static_cast<int>(N), w_codes, w_scales);
+  });
 }
 
 svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, int gelu, uint8_t* x_codes,
@@ -976,19 +1009,21 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
     return SVDQ_ERR_INVALID_ARG;
   if (K % 16 != 0 || ldx % 8 != 0 || M > kMaxRows || K > kMaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(X) || !aligned16(x_codes) || !aligned16(x_scales)) return SVDQ_ERR_MISALIGNED;
-  // rows a warp: one while that gives fewer than 64 warps an SM, else 4
-  const int dev = current_device();
-  if (dev < 0) return SVDQ_ERR_CUDA;
-  const int sms = sm_count(dev);
-  if (sms <= 0) return SVDQ_ERR_CUDA;
-  const int64_t segs = svdq::fp8_band_tiles(K);
-  const int rows = M * segs <= 64 * static_cast<int64_t>(sms) ? 1 : 4;
-  const int64_t warps = (M + rows - 1) / rows * segs;
-  const dim3 grid(static_cast<unsigned>((warps + svdq::kQ8Threads / 32 - 1) / (svdq::kQ8Threads / 32) + 1));
-  auto kern = rows == 1 ? (gelu ? svdq::quantize_fp8_kernel<1, true> : svdq::quantize_fp8_kernel<1, false>)
-                        : (gelu ? svdq::quantize_fp8_kernel<4, true> : svdq::quantize_fp8_kernel<4, false>);
-  return launch(kern, grid, svdq::kQ8Threads, 0, 1, stream, static_cast<const __nv_bfloat16*>(X), ldx,
-                static_cast<int>(M), static_cast<int>(K), aligned32(X) && ldx % 16 == 0, x_codes, x_scales);
+  return guarded([&] {
+    // rows a warp: one while that gives fewer than 64 warps an SM, else 4
+    const int dev = current_device();
+    if (dev < 0) return SVDQ_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SVDQ_ERR_CUDA;
+    const int64_t segs = svdq::fp8_band_tiles(K);
+    const int rows = M * segs <= 64 * static_cast<int64_t>(sms) ? 1 : 4;
+    const int64_t warps = (M + rows - 1) / rows * segs;
+    const dim3 grid(static_cast<unsigned>((warps + svdq::kQ8Threads / 32 - 1) / (svdq::kQ8Threads / 32) + 1));
+    auto kern = rows == 1 ? (gelu ? svdq::quantize_fp8_kernel<1, true> : svdq::quantize_fp8_kernel<1, false>)
+                          : (gelu ? svdq::quantize_fp8_kernel<4, true> : svdq::quantize_fp8_kernel<4, false>);
+    return launch(kern, grid, svdq::kQ8Threads, 0, 1, stream, static_cast<const __nv_bfloat16*>(X), ldx,
+                  static_cast<int>(M), static_cast<int>(K), aligned32(X) && ldx % 16 == 0, x_codes, x_scales);
+  });
 }
 
 svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int residual_dtype, const void* gamma,
@@ -1002,16 +1037,18 @@ svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int r
   for (const void* q : {X, residual, gamma, static_cast<const void*>(residual_out), static_cast<const void*>(Y),
                         static_cast<const void*>(x_codes), static_cast<const void*>(x_scales)})
     if (!aligned16(q)) return SVDQ_ERR_MISALIGNED;
-  return residual_dtype == SVDQ_F32
-             ? launch_rmsnorm<float>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales, stream)
-             : launch_rmsnorm<__nv_bfloat16>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales,
-                                             stream);
+  return guarded([&] {
+    return residual_dtype == SVDQ_F32
+               ? launch_rmsnorm<float>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales, stream)
+               : launch_rmsnorm<__nv_bfloat16>(X, ldx, residual, gamma, eps, M, K, residual_out, Y, x_codes, x_scales,
+                                               stream);
+  });
 }
 
 svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                             const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N, void* Y,
                             void* stream) {
-  return no_throw([&] {
+  return guarded([&] {
     return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, Y, nullptr, false, stream);
   });
 }
@@ -1019,7 +1056,7 @@ svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, con
 svdq_status svdq_linear_fp8_gelu(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
                                  const uint8_t* w_scales, const void* bias, int64_t M, int64_t K, int64_t N,
                                  uint8_t* y_codes, uint8_t* y_scales, void* stream) {
-  return no_throw([&] {
+  return guarded([&] {
     return linear_fp8_impl(x_codes, x_scales, w_codes, w_scales, bias, M, K, N, y_codes, y_scales, true, stream);
   });
 }
@@ -1034,60 +1071,63 @@ svdq_status svdq_attach_lora(const void* L1, const void* L2, const float* lambda
   if ((r > 0 && (!aligned16(L1) || !aligned16(L2))) || !aligned16(lambda) || !aligned16(A) || !aligned16(B) ||
       !aligned16(L1_out) || !aligned16(L2_out))
     return SVDQ_ERR_MISALIGNED;
-  const int dev = current_device();
-  if (dev < 0) return SVDQ_ERR_CUDA;
-  const int sms = sm_count(dev);
-  if (sms <= 0) return SVDQ_ERR_CUDA;
-  const int64_t chunks = K * ((r + ra) / 8) + (r + ra) * N / 8;
-  int64_t blocks = (chunks + svdq::kLoraThreads - 1) / svdq::kLoraThreads;
-  if (blocks > 8 * sms) blocks = 8 * sms;
-  svdq::attach_lora_kernel<<<static_cast<unsigned>(blocks), svdq::kLoraThreads, 0,
-                             static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const __nv_bfloat16*>(L1), static_cast<const __nv_bfloat16*>(L2), lambda,
-      static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), static_cast<int>(K),
-      static_cast<int>(N), static_cast<int>(r), static_cast<int>(ra), static_cast<__nv_bfloat16*>(L1_out),
-      static_cast<__nv_bfloat16*>(L2_out));
-  return launch_status();
+  return guarded([&] {
+    const int dev = current_device();
+    if (dev < 0) return SVDQ_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SVDQ_ERR_CUDA;
+    const int64_t chunks = K * ((r + ra) / 8) + (r + ra) * N / 8;
+    int64_t blocks = (chunks + svdq::kLoraThreads - 1) / svdq::kLoraThreads;
+    if (blocks > 8 * sms) blocks = 8 * sms;
+    return launch_plain(svdq::attach_lora_kernel, dim3(static_cast<unsigned>(blocks)), svdq::kLoraThreads, stream,
+                        static_cast<const __nv_bfloat16*>(L1), static_cast<const __nv_bfloat16*>(L2), lambda,
+                        static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B),
+                        static_cast<int>(K), static_cast<int>(N), static_cast<int>(r), static_cast<int>(ra),
+                        static_cast<__nv_bfloat16*>(L1_out), static_cast<__nv_bfloat16*>(L2_out));
+  });
 }
 
 svdq_status svdq_channel_absmax(const void* X, int64_t M, int64_t K, float* amax, void* stream) {
   if (!X || !amax || M <= 0 || K <= 0) return SVDQ_ERR_INVALID_ARG;
   if (K % 8 != 0 || K > kMaxK || M > kMaxRows) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(X) || !aligned16(amax)) return SVDQ_ERR_MISALIGNED;
-  const int dev = current_device();
-  if (dev < 0) return SVDQ_ERR_CUDA;
-  const int sms = sm_count(dev);
-  if (sms <= 0) return SVDQ_ERR_CUDA;
-  // enough row ranges for about four blocks per SM, at least 32 rows each
-  const int64_t col_blocks = (K / 8 + svdq::kAbsmaxThreads - 1) / svdq::kAbsmaxThreads;
-  int64_t row_blocks = (4 * static_cast<int64_t>(sms) + col_blocks - 1) / col_blocks;
-  if (row_blocks > (M + 31) / 32) row_blocks = (M + 31) / 32;
-  if (row_blocks > 65535) row_blocks = 65535;
-  const int64_t rows_per_block = (M + row_blocks - 1) / row_blocks;
-  row_blocks = (M + rows_per_block - 1) / rows_per_block;
-  const dim3 grid(static_cast<unsigned>(col_blocks), static_cast<unsigned>(row_blocks));
-  svdq::channel_absmax_kernel<<<grid, svdq::kAbsmaxThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const __nv_bfloat16*>(X), static_cast<int>(M), static_cast<int>(K),
-      static_cast<int>(rows_per_block), reinterpret_cast<unsigned int*>(amax));
-  return launch_status();
+  return guarded([&] {
+    const int dev = current_device();
+    if (dev < 0) return SVDQ_ERR_CUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SVDQ_ERR_CUDA;
+    // enough row ranges for about four blocks per SM, at least 32 rows each
+    const int64_t col_blocks = (K / 8 + svdq::kAbsmaxThreads - 1) / svdq::kAbsmaxThreads;
+    int64_t row_blocks = (4 * static_cast<int64_t>(sms) + col_blocks - 1) / col_blocks;
+    if (row_blocks > (M + 31) / 32) row_blocks = (M + 31) / 32;
+    if (row_blocks > 65535) row_blocks = 65535;
+    const int64_t rows_per_block = (M + row_blocks - 1) / row_blocks;
+    row_blocks = (M + rows_per_block - 1) / rows_per_block;
+    const dim3 grid(static_cast<unsigned>(col_blocks), static_cast<unsigned>(row_blocks));
+    return launch_plain(svdq::channel_absmax_kernel, grid, svdq::kAbsmaxThreads, stream,
+                        static_cast<const __nv_bfloat16*>(X), static_cast<int>(M), static_cast<int>(K),
+                        static_cast<int>(rows_per_block), reinterpret_cast<unsigned int*>(amax));
+  });
 }
 
 svdq_status svdq_sync_status(void* stream, int* where) {
   if (where) *where = 0;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SVDQ_ERR_CUDA;
-  unsigned int code = 0, w = 0;
-  if (cudaMemcpyFromSymbol(&code, svdq::g_status_code, sizeof(code)) != cudaSuccess ||
-      cudaMemcpyFromSymbol(&w, svdq::g_status_where, sizeof(w)) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  if (code != 0) {
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbol(svdq::g_status_code, &zero, sizeof(zero)) != cudaSuccess ||
-        cudaMemcpyToSymbol(svdq::g_status_where, &zero, sizeof(zero)) != cudaSuccess)
+  return guarded([&] {
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SVDQ_ERR_CUDA;
+    unsigned int code = 0, w = 0;
+    if (cudaMemcpyFromSymbol(&code, svdq::g_status_code, sizeof(code)) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&w, svdq::g_status_where, sizeof(w)) != cudaSuccess)
       return SVDQ_ERR_CUDA;
-    if (where) *where = static_cast<int>(w);
-    return static_cast<svdq_status>(code);
-  }
-  return SVDQ_OK;
+    if (code != 0) {
+      const unsigned int zero = 0;
+      if (cudaMemcpyToSymbol(svdq::g_status_code, &zero, sizeof(zero)) != cudaSuccess ||
+          cudaMemcpyToSymbol(svdq::g_status_where, &zero, sizeof(zero)) != cudaSuccess)
+        return SVDQ_ERR_CUDA;
+      if (where) *where = static_cast<int>(w);
+      return static_cast<svdq_status>(code);
+    }
+    return SVDQ_OK;
+  });
 }
 
 svdq_status svdq_set_wait_timeout(uint64_t timeout_ns) {
@@ -1116,8 +1156,7 @@ svdq_status svdq_set_launch_overlap(int enable) {
 
 svdq_status svdq_selftest_wait_timeout(uint64_t timeout_ns, void* stream) {
   if (timeout_ns == 0 || timeout_ns > 10000000000ull) return SVDQ_ERR_INVALID_ARG;
-  svdq::wait_timeout_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(timeout_ns);
-  return launch_status();
+  return guarded([&] { return launch_plain(svdq::wait_timeout_selftest_kernel, dim3(1), 32, stream, timeout_ns); });
 }
 
 // ------------------------------------------------ allocation-free variant --
@@ -1163,9 +1202,11 @@ svdq_status svdq_quantize_act_noalloc(const void* X, const float* inv_lambda, co
   if (need > kNoAllocScratchBytes) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   void* scratch = nullptr;
   if (need > 0) {
-    const int dev = current_device();
-    if (dev < 0) return SVDQ_ERR_CUDA;
-    if (svdq_status rc = noalloc_scratch(dev, &scratch)) return rc;
+    const svdq_status rc = guarded([&] {
+      const int dev = current_device();
+      return dev < 0 ? SVDQ_ERR_CUDA : noalloc_scratch(dev, &scratch);
+    });
+    if (rc) return rc;
   }
   return svdq_quantize_act(X, inv_lambda, L1, M, K, r, x_codes, x_scales, T, scratch, need ? kNoAllocScratchBytes : 0,
                            stream);

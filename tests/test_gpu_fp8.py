@@ -844,3 +844,67 @@ def test_rmsnorm_of_rows_near_the_bottom_of_fp32(eps):
         got, ok = _np(Y), np.abs(y) > 1e-30
         assert (got[ok] >= ref.bf16_round(y - err)[ok]).all() and (got[ok] <= ref.bf16_round(y + err)[ok]).all()
         assert np.abs(got[~ok]).max(initial=0.0) <= 1.01e-30
+
+
+def test_calls_do_not_report_an_error_of_somebody_else():
+    """A refused runtime call of the program's own, not yet looked at, is not
+    taken for the launch's; and it is left for its owner."""
+    import ctypes
+    torch, svdq = _m()
+    X = _dev(np.random.default_rng(1).normal(size=(4, 256)), torch.bfloat16)
+    W = _dev(np.random.default_rng(2).normal(size=(256, 64)), torch.bfloat16)
+    want = svdq.linear_fp8(*svdq.rmsnorm(X)[:2], *svdq.pack_weight_fp8(W))
+    _ok()
+    rt = ctypes.CDLL("libcudart.so.12")
+    W32 = W.float()
+    for call in (lambda: svdq.rmsnorm(X), lambda: svdq.quantize_fp8(X), lambda: svdq.pack_weight_fp8(W),
+                 lambda: svdq.pack_residual(W32)):
+        first = call()
+        assert rt.cudaSetDevice(-1) != 0                        # refused on the host: invalid device
+        got = call()
+        assert rt.cudaGetLastError() != 0 and rt.cudaGetLastError() == 0
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, first) if a is not None)
+    assert torch.equal(want, svdq.linear_fp8(*svdq.rmsnorm(X)[:2], *svdq.pack_weight_fp8(W)))
+    _ok()
+
+
+def test_a_failed_call_leaves_no_error_behind():
+    """A capture is ended by a synchronisation, so the calls into its stream are
+    refused by the runtime: each says so itself, and no later check of the
+    program (torch shares the runtime's last error) finds it again."""
+    import ctypes
+    torch, svdq = _m()
+    X = _dev(np.random.default_rng(1).normal(size=(4, 512)), torch.bfloat16)
+    wc, ws = svdq.pack_weight_fp8(_dev(np.random.default_rng(2).normal(size=(512, 64)), torch.bfloat16))
+    xc, xs = svdq.quantize_fp8(X)
+    Y = svdq.linear_fp8(xc, xs, wc, ws)
+    inv = torch.ones(512, device="cuda")
+    R = torch.ones((64, 16), device="cuda")
+    q4 = svdq.quantize_act(X, inv, None)
+    r4 = svdq.pack_residual(R)
+    c8, s8, y8 = xc.clone(), xs.clone(), Y.clone()
+    _ok()
+    rt = ctypes.CDLL("libcudart.so.12")
+    st = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(handle, 1) == 0             # this thread only
+    try:
+        assert svdq.sync_status(st)[0] == 4                      # not allowed in a capture, and ends it
+        assert rt.cudaGetLastError() == 0
+        for call in (lambda: svdq.quantize_fp8(X, c8, s8, stream=st),
+                     lambda: svdq.rmsnorm(X, x_codes=c8, x_scales=s8, stream=st),
+                     lambda: svdq.linear_fp8(xc, xs, wc, ws, Y=y8, stream=st),
+                     lambda: svdq.pack_residual(R, *r4, stream=st)):
+            with pytest.raises(svdq.SvdqError) as e:
+                call()
+            assert e.value.status == 4
+            assert rt.cudaGetLastError() == 0
+    finally:
+        assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+    got = svdq.linear_fp8(*svdq.quantize_fp8(X, stream=st), wc, ws, stream=st)
+    st.synchronize()
+    assert torch.equal(got, Y)
+    again = svdq.quantize_act(X, inv, None)
+    assert torch.equal(again[0], q4[0]) and torch.equal(again[1], q4[1])
+    _ok()
