@@ -213,8 +213,10 @@ __global__ void __launch_bounds__(kS8Threads)
   uint2 bw = make_uint2(0, 0);  // this lane's four channels, long before they are needed
   if (p.bias && n < p.N) bw = *reinterpret_cast<const uint2*>(p.bias + n);  // N is a multiple of 8
   // [bm][128], over the ring: once the MMAs are complete every stage that was
-  // loaded has been read.  (After an abort a copy may still land in it; the sums
-  // are not stored then.)
+  // loaded has been read.  (After an abort a copy may still land in it.  This
+  // CTA then stores nothing; the others of its cluster, which learn nothing of
+  // it, store sums with that part in them: outputs of a launch that records a
+  // timeout are undefined.)
   float* part = reinterpret_cast<float*>(ring);
   const int vrows = min(p.bm, p.M - m0);  // tokens of this tile
   if (warp >= 2 && !warp_wait(smem_u32(fin), 0, p.timeout_ns, 84)) {

@@ -370,7 +370,9 @@ svdq_status svdq_set_launch_overlap(int enable);
  * Failure detection.  Every wait inside the kernels is bounded (default
  * 2 s, or SVDQ_WAIT_TIMEOUT_MS from the environment at first use); a wait
  * that expires records SVDQ_ERR_TIMEOUT in the current device's status word
- * and the kernel returns without hanging the GPU.
+ * and the kernel returns without hanging the GPU.  The outputs of such a call
+ * are undefined: some parts are left as they were, others hold values of no
+ * use.
  *
  * svdq_sync_status synchronises `stream`, returns the recorded status of
  * the current device (SVDQ_OK if none; SVDQ_ERR_CUDA if the stream reports
