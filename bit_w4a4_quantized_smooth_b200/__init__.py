@@ -31,6 +31,7 @@ from .binding import (  # noqa: F401
     selftest_wait_timeout,
     set_launch_overlap,
     set_linear_fp8_path,
+    set_linear_fp8_splits,
     set_linear_path,
     set_wait_timeout,
     status_string,

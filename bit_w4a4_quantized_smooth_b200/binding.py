@@ -81,6 +81,8 @@ def load() -> ctypes.CDLL:
         L.svdq_fp8_sizes.argtypes = [_I64, _I64, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_size_t)]
         L.svdq_set_linear_fp8_path.restype = ctypes.c_int
         L.svdq_set_linear_fp8_path.argtypes = [ctypes.c_int]
+        L.svdq_set_linear_fp8_splits.restype = ctypes.c_int
+        L.svdq_set_linear_fp8_splits.argtypes = [ctypes.c_int]
         L.svdq_pack_weight_fp8.restype = ctypes.c_int
         L.svdq_pack_weight_fp8.argtypes = [_P, ctypes.c_int, _I64, _I64, _P, _P, _P]
         L.svdq_quantize_fp8.restype = ctypes.c_int
@@ -348,6 +350,11 @@ def set_linear_path(path: str):
 def set_linear_fp8_path(path: str):
     """Force the kernel of linear_fp8 and linear_fp8_gelu: "auto" (by shape), "large" or "small"."""
     _check(load().svdq_set_linear_fp8_path(LINEAR_PATHS[path]), "svdq_set_linear_fp8_path")
+
+
+def set_linear_fp8_splits(splits: int):
+    """Force the number of CTAs that share a tile in the few-rows kernel: 0 (by shape), or 1 to 8."""
+    _check(load().svdq_set_linear_fp8_splits(splits), "svdq_set_linear_fp8_splits")
 
 
 def set_launch_overlap(enable: bool):

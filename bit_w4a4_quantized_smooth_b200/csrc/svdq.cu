@@ -42,6 +42,9 @@ std::atomic<int> g_linear_path{0};
 // The same for svdq_linear_fp8 and svdq_linear_fp8_gelu (svdq_set_linear_fp8_path).
 std::atomic<int> g_linear8_path{0};
 
+// CTAs that share a tile of the few-rows kernel: 0 by estimate (svdq_set_linear_fp8_splits).
+std::atomic<int> g_linear8_splits{0};
+
 // Whether the layer's launches carry the programmatic stream-serialisation
 // attribute (svdq_set_launch_overlap; default on).  With it a layer kernel
 // may be scheduled while the kernel ahead of it in the stream finishes; it
@@ -437,7 +440,9 @@ int s8_active(int splits, size_t smem, int sms) {
 // average, 2 % at the worst for bf16 and 6 % with GELU (2 us a wave lost 41 %
 // at 512 x 12288 x 3072; a choice that does not count the GELU 8 % on average
 // and 62 % at the worst).  The deeper ring on ties.
-svdq_status s8_plan(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int dev, int sms) {
+// With `forced` splits only that many are considered, or the next smaller
+// number that leaves no CTA without stages.
+svdq_status s8_plan(S8Plan* out, bool gelu, int forced, int64_t M, int64_t K, int64_t N, int dev, int sms) {
   S8Plan best = {};
   const int bm = M >= svdq::kS8MaxBM ? svdq::kS8MaxBM : static_cast<int>((M + 15) / 16 * 16);
   const double x = bm / 128.0;
@@ -447,7 +452,13 @@ svdq_status s8_plan(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N, int
   const uint32_t tmem_cols = pow2_at_least(static_cast<uint32_t>(bm + 32));
   const void* model = reinterpret_cast<const void*>(svdq::linear_fp8_splitk_occupancy_kernel);
   if (svdq_status rc = ensure_smem(model, dev, svdq::kS8SmemLimit)) return rc;
-  for (int s = 1; s <= svdq::kS8MaxSplits && s <= k_stages; ++s) {
+  int first = 1, last = std::min(svdq::kS8MaxSplits, k_stages);
+  if (forced > 0) {
+    last = std::min(last, forced);
+    while ((k_stages + (k_stages + last - 1) / last - 1) / ((k_stages + last - 1) / last) != last) --last;
+    first = last;
+  }
+  for (int s = first; s <= last; ++s) {
     const int spc = (k_stages + s - 1) / s;
     const int passes = ((bm + s - 1) / s + 5) / 6;
     if ((k_stages + spc - 1) / spc != s) continue;  // no CTA without stages
@@ -491,7 +502,10 @@ svdq_status s8_plan_kept(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N
   // M only through its tile count and padded tile
   const uint64_t m_class = M >= svdq::kS8MaxBM ? static_cast<uint64_t>((M + 127) / 128) << 8
                                                : static_cast<uint64_t>((M + 15) / 16);
-  const S8Key key = {{m_class | static_cast<uint64_t>(gelu) << 47 | static_cast<uint64_t>(dev) << 48, static_cast<uint64_t>(K), static_cast<uint64_t>(N)}};
+  const int forced = g_linear8_splits.load(std::memory_order_relaxed);
+  const S8Key key = {{m_class | static_cast<uint64_t>(forced) << 40 | static_cast<uint64_t>(gelu) << 47 |
+                          static_cast<uint64_t>(dev) << 48,
+                      static_cast<uint64_t>(K), static_cast<uint64_t>(N)}};
   {
     std::lock_guard<std::mutex> lock(g_s8_mu);
     auto it = g_s8_plans.find(key);
@@ -500,7 +514,7 @@ svdq_status s8_plan_kept(S8Plan* out, bool gelu, int64_t M, int64_t K, int64_t N
       return SVDQ_OK;
     }
   }
-  if (svdq_status rc = s8_plan(out, gelu, M, K, N, dev, sms)) return rc;
+  if (svdq_status rc = s8_plan(out, gelu, forced, M, K, N, dev, sms)) return rc;
   std::lock_guard<std::mutex> lock(g_s8_mu);
   if (g_s8_plans.size() >= kMapCacheCap) g_s8_plans.clear();
   g_s8_plans.emplace(key, *out);
@@ -1145,6 +1159,12 @@ svdq_status svdq_set_linear_path(int path) {
 svdq_status svdq_set_linear_fp8_path(int path) {
   if (path < 0 || path > 2) return SVDQ_ERR_INVALID_ARG;
   g_linear8_path.store(path, std::memory_order_relaxed);
+  return SVDQ_OK;
+}
+
+svdq_status svdq_set_linear_fp8_splits(int splits) {
+  if (splits < 0 || splits > svdq::kS8MaxSplits) return SVDQ_ERR_INVALID_ARG;
+  g_linear8_splits.store(splits, std::memory_order_relaxed);
   return SVDQ_OK;
 }
 

@@ -349,6 +349,11 @@ svdq_status svdq_set_linear_path(int path);
  * split over a cluster).  Both compute the same sums in another order. */
 svdq_status svdq_set_linear_fp8_path(int path);
 
+/* CTAs that share K of a tile in the few-rows kernel (host-side setting for the
+ * whole process): 0 by shape (default), 1 to 8 that many, or the next smaller
+ * number that gives each of them a part of K.  The sums' order depends on it. */
+svdq_status svdq_set_linear_fp8_splits(int splits);
+
 /*
  * Launch overlap of the layer calls (host-side setting for the whole
  * process; 1 by default).  With 1, svdq_quantize_act(_gelu, _noalloc) and

@@ -93,6 +93,15 @@ def test_path_setting(lib):
     set_linear_fp8_path("auto")
 
 
+def test_splits_setting(lib):
+    from bit_w4a4_quantized_smooth_b200 import SvdqError, set_linear_fp8_splits
+    assert lib.svdq_set_linear_fp8_splits(9) == 1 and lib.svdq_set_linear_fp8_splits(-1) == 1
+    with pytest.raises(SvdqError):
+        set_linear_fp8_splits(9)
+    set_linear_fp8_splits(8)
+    set_linear_fp8_splits(0)
+
+
 def test_binding_refuses_what_the_abi_cannot_see():
     """Types, shapes, strides and devices are checked before a pointer is taken."""
     import torch

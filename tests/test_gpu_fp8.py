@@ -908,3 +908,51 @@ def test_a_failed_call_leaves_no_error_behind():
     again = svdq.quantize_act(X, inv, None)
     assert torch.equal(again[0], q4[0]) and torch.equal(again[1], q4[1])
     _ok()
+
+
+@pytest.fixture(params=range(1, 9))
+def splits(request):
+    _, svdq = _m()
+    svdq.set_linear_fp8_path("small")
+    svdq.set_linear_fp8_splits(request.param)
+    yield request.param
+    svdq.set_linear_fp8_splits(0)
+    svdq.set_linear_fp8_path("auto")
+
+
+@pytest.mark.parametrize("M", [1, 21, 64, 77, 128, 200])
+def test_linear_few_rows_with_every_split(M, splits):
+    """One to eight CTAs share a tile (56 stages along K: each number divides
+    them so that none is left without any), up to and above the 64 tokens from
+    which several tokens' partials are added at a time; K, N and the last tile
+    of tokens end inside a tile."""
+    torch, svdq = _m()
+    K = 7056                                                   # 55 stages and a short one
+    gen = torch.Generator(device="cuda").manual_seed(8 * M + splits)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = svdq.quantize_fp8((rand(M, K) * torch.exp(rand(M, 1))).bfloat16())
+    for N in (280, 272):
+        w = svdq.pack_weight_fp8((rand(K, N) / K ** 0.5).bfloat16())
+        b = rand(N).bfloat16()
+        Y = svdq.linear_fp8(*x, *w, b)
+        _ok()
+        xv = torch.from_numpy(ref.decode(_np(x[0]), ref.untile(_np(x[1]), M, K)[0])).cuda()
+        wv = torch.from_numpy(ref.decode(_np(w[0]), ref.untile(_np(w[1]), N, K)[0])).cuda()
+        y = (xv @ wv.T + b.double()).cpu().numpy()
+        acc = (-(-K // 32) + splits) * 2.0 ** -23 * (xv.abs() @ wv.abs().T + b.double().abs()).cpu().numpy()
+        _check_y(Y, y, acc)
+        if N % 16 == 0:
+            codes, scales = svdq.linear_fp8_gelu(*x, *w, b)
+            _ok()
+            g = ref.gelu(y)
+            ref.assert_encodes(_np(codes), _np(scales), g, 1.13 * acc + np.abs(g) * GELU_REL)
+
+
+def test_linear_few_rows_with_more_splits_than_stages(splits):
+    """The next smaller number that leaves no CTA without a part of K: 5 stages
+    are shared by 5, 3 (2 + 2 + 1), 2 or 1, and 1 stage by nobody."""
+    torch, svdq = _m()
+    for K in (592, 16):
+        ten, y, acc = _layer(np.random.default_rng(K + splits), 9, K, 136, True)
+        _check_y(svdq.linear_fp8(*ten), y, acc + 7 * acc / (-(-K // 32) + 1))
+    _ok()
