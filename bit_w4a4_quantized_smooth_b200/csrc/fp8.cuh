@@ -16,9 +16,7 @@ namespace svdq {
 
 constexpr int kFp8Block = 128;
 
-// Blocks per row, and the 512-byte scale tiles (128 rows x 4 blocks) per
-// 128-row band.
-__host__ __device__ __forceinline__ int64_t fp8_blocks(int64_t K) { return (K + 127) >> 7; }
+// 512-byte scale tiles (128 rows x 4 blocks) per 128-row band.
 __host__ __device__ __forceinline__ int64_t fp8_band_tiles(int64_t K) { return (K + 511) >> 9; }
 
 // Byte offset of the scale of (row, block) in the tile layout; the four
@@ -286,10 +284,6 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[6] = b.z;
   v[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                            pack_bf16x2(v[6], v[7]));
-}
 __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -433,10 +427,12 @@ __global__ void __launch_bounds__(kQ8Threads)
 // Rounding.  1 / sqrt(...) is carried as a sum of two fp32 numbers, h gamma is
 // exact (two 8-bit significands; with an fp32 residual its error is carried
 // along), and y = h gamma (r_hi + r_lo) is one fused operation rounded toward
-// zero with its last bit set to mark what was cut off.  The one rounding that
-// counts, to E4M3 or bf16, is then that of the exact product: an fp32 product
-// rounded to nearest would land on an E4M3 tie for one value in a million and
-// turn half of those the wrong way.
+// zero with its last bit set to mark what was cut off.  Given r, the product is
+// then rounded once, to E4M3 or bf16: an fp32 product rounded to nearest would
+// land on an E4M3 tie for one value in a million and turn half of those the
+// wrong way.  r itself carries half the relative error of the fp32 sum of
+// squares (tens of 2^-24 at the most); its second word keeps the root and the
+// division from adding to that.
 constexpr int kNormMaxThreads = 512;
 
 // 1 / sqrt(sum / K + eps) as hi + lo.  lo is 0 where hi^2 leaves fp32's range:
