@@ -278,7 +278,10 @@ def _native():
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing: build it with `python -m bit_w4a4_quantized_smooth_b200.build`")
         import torch  # noqa: F401  (its libraries are what the module is linked to)
-        from . import _svdq_torch
+        from . import _svdq_torch, build
+        if _svdq_torch.built_for != build.torch_tag():
+            raise ImportError(f"{path} was built for {_svdq_torch.built_for}, this is {build.torch_tag()}: build it "
+                              f"with `python -m bit_w4a4_quantized_smooth_b200.build`")
         _svdq_torch.set_error(SvdqError)
         _ext = _svdq_torch
     return _ext

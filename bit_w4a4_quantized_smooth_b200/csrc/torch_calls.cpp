@@ -357,4 +357,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_svdq_torch", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__svdq_torch() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__svdq_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", SVDQ_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
