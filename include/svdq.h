@@ -248,7 +248,8 @@ svdq_status svdq_channel_absmax(const void* X, int64_t M, int64_t K, float* amax
  *    +-448 2^120.
  * Conventions as above, with these sizes: K a multiple of 16, N a multiple of
  * 8 (16 for svdq_linear_fp8_gelu), M >= 1.  NaN and infinity are allowed: a
- * NaN stays in its row.  No call needs a workspace, outputs overlap inputs
+ * NaN stays in its row (an infinite h makes its element of the norm NaN and the
+ * rest of its row zeros, as the formula does).  No call needs a workspace, outputs overlap inputs
  * only where that is said, and a call repeated on equal inputs gives equal
  * bits (the order of the sums depends on M, K and N).  The scale byte 255 is
  * NaN. */
@@ -294,7 +295,8 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
  * sum of squares exceeds 2^128 gives zeros.
  *   X             bf16 [M][K], row stride ldx (ldx >= K, a multiple of 8)
  *   residual      [M][K] of residual_dtype (an svdq_dtype), or NULL
- *   gamma         bf16 [K], or NULL for ones
+ *   gamma         bf16 [K], or NULL for ones; finite, and |h gamma| below 2^128
+ *                 (an element beyond gives NaN)
  *   eps           >= 0, finite (with 0, a row of zeros gives NaN, and one that
  *                 counts as such infinities or NaN)
  *   residual_out  [M][K] of residual_dtype: h (NULL iff residual is); may be

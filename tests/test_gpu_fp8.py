@@ -956,3 +956,112 @@ def test_linear_few_rows_with_more_splits_than_stages(splits):
         ten, y, acc = _layer(np.random.default_rng(K + splits), 9, K, 136, True)
         _check_y(svdq.linear_fp8(*ten), y, acc + 7 * acc / (-(-K // 32) + 1))
     _ok()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_pack_weight_special_values(dt):
+    """A NaN is the code NaN and leaves its block's scale alone; an infinity is
+    +-448 with the largest scale; both stay in their channel and block."""
+    torch, svdq = _m()
+    K, N = 272, 24
+    W = _dev(np.random.default_rng(6).normal(size=(K, N)), torch.bfloat16 if dt == "bf16" else torch.float32)
+    plain, plain_s = svdq.pack_weight_fp8(W)
+    V = W.clone()
+    V[3, 1] = V[130, 5] = float("nan")
+    V[128:256, 2] = float("nan")                               # a whole block
+    V[7, 9], V[271, 10] = float("inf"), float("-inf")
+    codes, scales = svdq.pack_weight_fp8(V)
+    _ok()
+    c, p = _np(codes), _np(plain)
+    s, rest = ref.untile(_np(scales), N, K)
+    sp, _ = ref.untile(_np(plain_s), N, K)
+    assert not _np(scales)[rest].any()
+    nan = np.zeros((N, K), dtype=bool)
+    nan[1, 3] = nan[5, 130] = True
+    nan[2, 128:256] = True
+    assert np.array_equal(np.isnan(ref.E4M3[c]), nan)
+    assert s[9, 0] == s[10, 2] == 247 and s[2, 1] == 0
+    assert ref.E4M3[c[9, 7]] == 448 and ref.E4M3[c[10, 271]] == -448
+    assert not ref.E4M3[c[9, :7]].any() and not ref.E4M3[c[10, 256:271]].any()
+    same = np.ones((N, 3), dtype=bool)                         # blocks whose scale is an amax of what is left
+    same[9, 0] = same[10, 2] = same[2, 1] = False
+    v = _np(V).T.copy()
+    v[np.isnan(v)] = 0.0
+    v[9, :128] = v[10, 256:] = 0.0
+    want, ws = ref.encode(v)
+    assert np.array_equal(s[same], ws[same])
+    keep = np.repeat(same, 128, axis=1)[:, :K] & ~nan
+    assert np.array_equal(c[keep], want[keep])
+    others = [0, 3, 4, 6, 7, 8] + list(range(11, N))
+    assert np.array_equal(c[others], p[others]) and np.array_equal(s[others], sp[others])
+
+
+@pytest.mark.parametrize("res", ["none", "bf16", "f32"])
+def test_rmsnorm_of_infinities(res):
+    """An infinite h: inf / inf is NaN in its element, and the rest of its row is
+    divided by infinity.  An infinite or overflowing gamma: NaN in its column.
+    The other rows are what they are without."""
+    torch, svdq = _m()
+    K = 400
+    X = _dev(np.random.default_rng(7).normal(size=(5, K)), torch.bfloat16)
+    R = None if res == "none" else torch.ones((5, K), dtype=torch.float32 if res == "f32" else torch.bfloat16, device="cuda")
+    plain = svdq.rmsnorm(X, None, R, bf16_out=True)
+    V = X.clone()
+    V[1, 5], V[3, 300] = float("inf"), float("-inf")
+    codes, scales, h, Y = svdq.rmsnorm(V, None, R, bf16_out=True)
+    _ok()
+    v, y = ref.E4M3[_np(codes)], _np(Y)
+    s, rest = ref.untile(_np(scales), 5, K)
+    assert not _np(scales)[rest].any() and not s[1].any() and not s[3].any()
+    for row, col in ((1, 5), (3, 300)):
+        assert np.isnan(v[row, col]) and np.isnan(y[row, col])
+        assert not np.delete(v[row], col).any() and not np.delete(y[row], col).any()
+    ok = [0, 2, 4]
+    assert np.array_equal(_np(codes)[ok], _np(plain[0])[ok]) and torch.equal(Y[ok], plain[3][ok])
+    if h is not None:
+        assert h[1, 5] == float("inf") and h[3, 300] == float("-inf")
+    G = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    G[17] = float("inf")
+    Y = svdq.rmsnorm(X, G, R, fp8_out=False, bf16_out=True)[3]
+    _ok()
+    assert torch.isnan(Y[:, 17]).all() and torch.isnan(Y).sum() == 5
+    Y[:, 17] = plain[3][:, 17]
+    assert torch.equal(Y, plain[3])
+
+
+def test_linear_of_nan_and_large_scales(path):
+    """The scale byte 255 is NaN: of x it takes its token, of w its channel.
+    Products beyond bf16 and fp32 are infinite, and 448 2^120 as FP8."""
+    torch, svdq = _m()
+    rng = np.random.default_rng(8)
+    for M in (5, 150):
+        K, N = 640, 272
+        (xc, xs, wc, ws, b), y, acc = _layer(rng, M, K, N, True)
+        at = lambda row, blk: (blk // 4) * 512 + (row % 32) * 16 + (row % 128) // 32 * 4 + blk % 4  # of the first band
+        xs, ws = xs.view(torch.uint8).clone(), ws.view(torch.uint8).clone()
+        xs[at(3, 2)] = 255
+        ws[at(40, 4)] = 255
+        Y = svdq.linear_fp8(xc, xs, wc, ws, b)
+        codes, scales = svdq.linear_fp8_gelu(xc, xs, wc, ws, b)
+        _ok()
+        nan = np.zeros((M, N), dtype=bool)
+        nan[3], nan[:, 40] = True, True
+        assert np.array_equal(np.isnan(_np(Y)), nan)
+        assert np.array_equal(np.isnan(ref.E4M3[_np(codes)]), nan)
+        _check_y(torch.where(torch.from_numpy(nan).cuda(), 0.0, Y), np.where(nan, 0.0, y), acc)
+        keep = np.array([r for r in range(M) if r != 3])
+        s, _ = ref.untile(_np(scales), M, N)
+        g = np.where(nan, 0.0, ref.gelu(y))[keep]              # a NaN does not change its block's scale
+        c = np.where(nan, 0, _np(codes)).astype(np.uint8)[keep]
+        ref.assert_encodes(c, ref.tiles(s[keep]), g, 1.13 * acc[keep] + np.abs(g) * GELU_REL)
+    x = torch.full((2, 256), 3e38, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((256, 256), dtype=torch.float32, device="cuda")
+    w[0, 0], w[0, 1], w[0, 2] = 2.0, -2.0, 1.0
+    q, p = svdq.quantize_fp8(x), svdq.pack_weight_fp8(w)
+    Y = svdq.linear_fp8(*q, *p)
+    codes, scales = svdq.linear_fp8_gelu(*q, *p)
+    _ok()
+    assert (Y[:, 0] == float("inf")).all() and (Y[:, 1] == float("-inf")).all() and torch.isfinite(Y[:, 2]).all()
+    assert not Y[:, 3:].any()
+    v, s = ref.E4M3[_np(codes)], ref.untile(_np(scales), 2, 256)[0]
+    assert (s[:, 0] == 247).all() and (v[:, 0] == 448).all() and not v[:, 1].any() and not v[:, 3:].any()
