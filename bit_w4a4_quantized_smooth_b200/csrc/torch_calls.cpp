@@ -190,6 +190,14 @@ struct Fp8Out {
   uint8_t* s() const { return static_cast<uint8_t*>(ptr(scales)); }
 };
 
+// Outputs that the caller gave have been written to: autograd's version counter
+// of each goes up, as after any in-place operation, so that a backward pass
+// that saved one of them notices.  (Inference tensors have none.)
+void written(std::initializer_list<const Opt*> outs) {
+  for (const Opt* t : outs)
+    if (*t && !(*t)->is_inference()) (*t)->unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const Opt& t) {
   if (t) return THPVariable_Wrap(*t);
   Py_RETURN_NONE;
@@ -234,6 +242,7 @@ PyObject* pack_weight(PyObject* const* a) {
     return svdq_pack_weight_fp8(W.data_ptr(), W.scalar_type() == at::kFloat ? SVDQ_F32 : SVDQ_BF16, K, N, out.c(),
                                 out.s(), st);
   });
+  written({&out.codes, &out.scales});
   return tuple({&out.codes, &out.scales});
 }
 
@@ -247,6 +256,7 @@ PyObject* quantize(PyObject* const* a) {
     out.fill();
     return svdq_quantize_fp8(X.data_ptr(), r.ld, r.M, r.K, gelu, out.c(), out.s(), st);
   });
+  written({&out.codes, &out.scales});
   return tuple({&out.codes, &out.scales});
 }
 
@@ -289,6 +299,7 @@ PyObject* rmsnorm(PyObject* const* a) {
                         residual && residual->scalar_type() == at::kFloat ? SVDQ_F32 : SVDQ_BF16, ptr(gamma),
                         static_cast<float>(eps), r.M, r.K, ptr(residual_out), ptr(Y), out.c(), out.s(), st);
   });
+  written({&out.codes, &out.scales, &residual_out, &Y});
   return tuple({&out.codes, &out.scales, &residual_out, &Y});
 }
 
@@ -323,6 +334,7 @@ PyObject* linear(PyObject* const* a) {
     if (!Y) make_outputs(Wanted{&Y, l.M, l.N, at::kBFloat16});
     return svdq_linear_fp8(l.u8(l.xc), l.u8(l.xs), l.u8(l.wc), l.u8(l.ws), ptr(l.bias), l.M, l.K, l.N, ptr(Y), st);
   });
+  written({&Y});
   return wrap(Y);
 }
 
@@ -335,6 +347,7 @@ PyObject* linear_gelu(PyObject* const* a) {
     return svdq_linear_fp8_gelu(l.u8(l.xc), l.u8(l.xs), l.u8(l.wc), l.u8(l.ws), ptr(l.bias), l.M, l.K, l.N, out.c(),
                                 out.s(), st);
   });
+  written({&out.codes, &out.scales});
   return tuple({&out.codes, &out.scales});
 }
 

@@ -1065,3 +1065,36 @@ def test_linear_of_nan_and_large_scales(path):
     assert not Y[:, 3:].any()
     v, s = ref.E4M3[_np(codes)], ref.untile(_np(scales), 2, 256)[0]
     assert (s[:, 0] == 247).all() and (v[:, 0] == 448).all() and not v[:, 1].any() and not v[:, 3:].any()
+
+
+def test_given_outputs_are_seen_by_autograd_as_written():
+    """A tensor saved for a backward pass and then given as an output: the pass
+    is refused, as after any in-place operation.  Inference tensors may be given."""
+    torch, svdq = _m()
+    z = lambda *s, d=torch.bfloat16: torch.zeros(s, dtype=d, device="cuda")
+    X = torch.ones((4, 256), dtype=torch.bfloat16, device="cuda")
+    wc, ws = svdq.pack_weight_fp8(z(256, 32))
+    xc, xs = svdq.quantize_fp8(X)
+    R, Y, Y2 = z(4, 256), z(4, 256), z(4, 32)
+    for out, call in ((R, lambda: svdq.rmsnorm(X, None, R, residual_out=R)), (Y, lambda: svdq.rmsnorm(X, Y=Y)),
+                      (Y2, lambda: svdq.linear_fp8(xc, xs, wc, ws, Y=Y2))):
+        a = torch.ones_like(out, requires_grad=True)
+        loss = (a * out).sum()
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    c, s = z(4, 256, d=torch.uint8), z(512, d=torch.uint8)
+    hc, hs = z(4, 32, d=torch.uint8), z(512, d=torch.uint8)
+    pc, ps = z(32, 256, d=torch.uint8), z(512, d=torch.uint8)
+    for outs, call in (((c, s), lambda: svdq.quantize_fp8(X, c, s)), ((c, s), lambda: svdq.rmsnorm(X, x_codes=c, x_scales=s)),
+                       ((pc, ps), lambda: svdq.pack_weight_fp8(z(256, 32), pc, ps)),
+                       ((hc, hs), lambda: svdq.linear_fp8_gelu(xc, xs, wc, ws, None, hc, hs))):
+        before = [t._version for t in outs]
+        call()
+        assert [t._version for t in outs] == [v + 1 for v in before]
+    with torch.inference_mode():
+        I = z(4, 32)
+    assert svdq.linear_fp8(xc, xs, wc, ws, Y=I) is I
+    with torch.inference_mode():
+        assert svdq.linear_fp8(xc, xs, wc, ws, Y=I) is I and svdq.rmsnorm(X, Y=Y)[3] is Y
+    _ok()
