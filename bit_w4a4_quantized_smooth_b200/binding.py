@@ -264,7 +264,8 @@ def channel_absmax(X, amax=None, stream=None):
 # which allocates the outputs that are not given (on the stream that writes
 # them; codes and scales share an allocation, as do all outputs of a call that
 # need 1 MiB or less) and makes the C ABI's call on the device of the first
-# argument, on that device's current stream unless one is given.  Forward only: no gradients are recorded.
+# argument, on that device's current stream unless one is given.  Outputs are
+# made past torch's dispatcher, so its modes do not see these calls.
 
 _ext = None
 
@@ -296,13 +297,15 @@ def fp8_sizes(rows: int, K: int) -> Tuple[int, int]:
 
 
 def pack_weight_fp8(W, w_codes=None, w_scales=None, stream=None):
-    """W bf16 or fp32 [K][N] -> (w_codes float8_e4m3fn [N][K], w_scales)."""
+    """W bf16 or fp32 [K][N] -> (w_codes float8_e4m3fn [N][K], w_scales).
+    Forward only: the outputs carry no gradient, whatever the inputs do."""
     return (_ext or _native()).pack_weight_fp8(W, w_codes, w_scales, stream)
 
 
 def quantize_fp8(X, x_codes=None, x_scales=None, stream=None, gelu: bool = False):
     """X bf16 [M][K] (rows may be strided) -> (x_codes float8_e4m3fn [M][K],
-    x_scales) of X, or of GELU(X)."""
+    x_scales) of X, or of GELU(X).  Forward only: the outputs carry no
+    gradient, whatever X does."""
     return (_ext or _native()).quantize_fp8(X, x_codes, x_scales, stream, gelu)
 
 
@@ -313,20 +316,23 @@ def rmsnorm(X, gamma=None, residual=None, eps: float = 1e-6, residual_out=None, 
     fp8_out=False), h in the residual's type (bf16 or fp32; None without a
     residual; pass residual_out=residual to update it in place), y as bf16
     (with bf16_out=True or a given Y).  X bf16 [M][K] (rows may be strided),
-    gamma bf16 [K]."""
+    gamma bf16 [K].  Forward only: the outputs carry no gradient, whatever the
+    inputs do."""
     return (_ext or _native()).rmsnorm(X, gamma, residual, eps, residual_out, Y, x_codes, x_scales, fp8_out, bf16_out,
                                        stream)
 
 
 def linear_fp8(x_codes, x_scales, w_codes, w_scales, bias=None, Y=None, stream=None):
     """8-bit linear: x_codes [M][K], w_codes [N][K] with their scales, bias
-    bf16 [N] or None -> Y bf16 [M][N]."""
+    bf16 [N] or None -> Y bf16 [M][N].  Forward only: Y carries no gradient,
+    whatever the inputs do."""
     return (_ext or _native()).linear_fp8(x_codes, x_scales, w_codes, w_scales, bias, Y, stream)
 
 
 def linear_fp8_gelu(x_codes, x_scales, w_codes, w_scales, bias=None, y_codes=None, y_scales=None, stream=None):
     """8-bit linear with GELU and the next layer's quantiser in its epilogue
-    -> (y_codes float8_e4m3fn [M][N], y_scales)."""
+    -> (y_codes float8_e4m3fn [M][N], y_scales).  Forward only: the outputs
+    carry no gradient, whatever the inputs do."""
     return (_ext or _native()).linear_fp8_gelu(x_codes, x_scales, w_codes, w_scales, bias, y_codes, y_scales, stream)
 
 

@@ -311,7 +311,11 @@ svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int r
                          uint8_t* x_scales, void* stream);
 
 /*
- * 8-bit linear: Y = deq(x) deq(w)^T + bias as bf16.
+ * 8-bit linear: Y = deq(x) deq(w)^T + bias as bf16.  The products are exact and
+ * summed by the tensor cores in fp32, which cut off toward zero: a sum is off by
+ * at most (ceil(K / 32) + 8) 2^-23 of its terms' absolute sum, and on average by
+ * 1.6e-7 of the result's norm at K = 3072 and 8.2e-7 at K = 12288 (an fp32
+ * product that rounds to nearest: 0.7e-7 and 1.6e-7).
  *   x_codes, x_scales   FP8 block-128 of M rows of length K
  *   w_codes, w_scales   from svdq_pack_weight_fp8 (N rows)
  *   bias                bf16 [N] or NULL (added in fp32)
@@ -324,7 +328,8 @@ svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, con
 /*
  * 8-bit linear whose epilogue is the next layer's activation step:
  * GELU(deq(x) deq(w)^T + bias), taken in fp32 (GELU as svdq_quantize_fp8), to
- * FP8 block-128 along N.
+ * FP8 block-128 along N.  The sum as in svdq_linear_fp8: its error moves about 5
+ * codes in a million to a neighbour at K = 3072.
  *   y_codes   uint8 [M][N] output;   y_scales   svdq_fp8_sizes(M, N) output
  * N a multiple of 16, N <= 2^20.
  */
