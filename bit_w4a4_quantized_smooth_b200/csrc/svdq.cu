@@ -641,9 +641,12 @@ template <typename RES>
 svdq_status launch_rmsnorm(const void* X, int64_t ldx, const void* residual, const void* gamma, float eps, int64_t M,
                            int64_t K, void* residual_out, void* Y, uint8_t* x_codes, uint8_t* x_scales, void* stream) {
   // One segment of 512 columns a warp as far as 16 warps reach; two where
-  // there are rows enough to fill the SMs several times (4608 x 3072 on B200:
-  // 18.1 us against 18.6; 512 x 4096: 6.3 against 5.6; with an fp32 residual
-  // one stays better, 26.6 against 27.7 us).  A row of one warp: four a CTA.
+  // there are rows enough to fill the SMs several times.  Measured on B200 at
+  // K = 4096 with a bf16 residual and FP8 output, one against two, by segments
+  // an SM: 5.9 and 6.6 us at 40, 11.6 and 11.8 at 100, 14.1 and 14.0 at 130,
+  // 16.5 and 16.2 at 160, 28.3 and 27.2 at 300, 86.8 and 79.6 at 1000 (K = 1024
+  // and 3072 within 3 % of that).  With an fp32 residual one stays better, 28.9
+  // and 30.0 at 200, 64.5 and 65.4 at 500.  A row of one warp: four a CTA.
   const int dev = current_device();
   if (dev < 0) return SVDQ_ERR_CUDA;
   const int sms = sm_count(dev);
@@ -1024,13 +1027,17 @@ svdq_status svdq_quantize_fp8(const void* X, int64_t ldx, int64_t M, int64_t K, 
   if (K % 16 != 0 || ldx % 8 != 0 || M > kMaxRows || K > kMaxK) return SVDQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(X) || !aligned16(x_codes) || !aligned16(x_scales)) return SVDQ_ERR_MISALIGNED;
   return guarded([&] {
-    // rows a warp: one while that gives fewer than 64 warps an SM, else 4
+    // Rows a warp: one while that gives at most 128 warps an SM, else 4.  On
+    // B200 at K = 3072, one row against four, by warps an SM with one row: 4.2
+    // and 4.9 us at 64 (with GELU 5.7 and 7.7), 5.4 and 5.6 at 96 (7.8 and 8.3),
+    // 6.7 and 6.6 at 128 (10.1 and 11.1; 10.1 and 9.8 at K = 512), 11.5 and 10.5
+    // at 256 (17.9 and 16.5), 21.2 and 19.1 at 512 (33.9 and 29.3).
     const int dev = current_device();
     if (dev < 0) return SVDQ_ERR_CUDA;
     const int sms = sm_count(dev);
     if (sms <= 0) return SVDQ_ERR_CUDA;
     const int64_t segs = svdq::fp8_band_tiles(K);
-    const int rows = M * segs <= 64 * static_cast<int64_t>(sms) ? 1 : 4;
+    const int rows = M * segs <= 128 * static_cast<int64_t>(sms) ? 1 : 4;
     const int64_t warps = (M + rows - 1) / rows * segs;
     const dim3 grid(static_cast<unsigned>((warps + svdq::kQ8Threads / 32 - 1) / (svdq::kQ8Threads / 32) + 1));
     auto kern = rows == 1 ? (gelu ? svdq::quantize_fp8_kernel<1, true> : svdq::quantize_fp8_kernel<1, false>)

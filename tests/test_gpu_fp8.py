@@ -1098,3 +1098,16 @@ def test_given_outputs_are_seen_by_autograd_as_written():
     with torch.inference_mode():
         assert svdq.linear_fp8(xc, xs, wc, ws, Y=I) is I and svdq.rmsnorm(X, Y=Y)[3] is Y
     _ok()
+
+
+@pytest.mark.parametrize("M,K", [(9481, 528), (1583, 6160), (9470, 528)])
+def test_quantize_gelu_many_rows(M, K):
+    """Enough rows that a warp takes four (not so in the last): rows and columns end inside its share."""
+    torch, svdq = _m()
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    X = (torch.randn((M, K), generator=gen, device="cuda") * 2.0).bfloat16()
+    X[:, 128:256] -= 8.0                                       # blocks without a value above 0.3
+    codes, scales = svdq.quantize_fp8(X, gelu=True)
+    _ok()
+    g = ref.gelu(_np(X))
+    ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
