@@ -342,10 +342,11 @@ __device__ __forceinline__ void zero_tile_scales(uint8_t* scales, int rows, int6
 // tile's four blocks) of R consecutive rows: a lane holds 16 columns of each
 // row (32 bytes a row, all R rows' in flight before the first is used: 128
 // bytes a thread at R = 4), 8 lanes a block; a row's four scale
-// bytes leave as one word.  On B200 4608 x 12288 of 21504 columns take 23.4 us
-// (170 MB, of which the codes largely stay in L2), with GELU 41.2: there the
-// polynomial bounds it (arithmetic pipes 57 and 54 % busy, issue 67 %).  64 x
-// 15360 take 4.1 us a call, which is the host's pace.  (A first version with 8
+// bytes leave as one word.  On B200 4608 x 12288 of 21504 columns take 23.3 us
+// (170 MB, of which the codes largely stay in L2), with GELU 40.3: there a
+// warp's loads and its polynomial alternate (arithmetic pipes 57 and 54 % busy,
+// issue 67 %).  64 x 15360 take 4.3 us a call, which is the host's pace (3.0 in
+// a graph).  (A first version with 8
 // columns a lane, 4 rows and single scale bytes took 43.1 us, 59.4 with GELU:
 // half the loads in flight, and 2.7 us for the byte stores.)
 // The grid's last block zeroes the padding rows' scales.
@@ -417,9 +418,9 @@ __global__ void __launch_bounds__(kQ8Threads)
 //
 // A warp takes 512 columns (16 a lane, 8 lanes a block) of one row at a time,
 // S such segments in registers (h as packed bf16 where that is its type);
-// `wpr` warps share a row.  On B200 4608 x 3072 take 19.3 us (99 MB: 5.1 TB/s,
+// `wpr` warps share a row.  On B200 4608 x 3072 take 19.4 us (99 MB: 5.1 TB/s,
 // 78 % of a copy; issue 62 %, and a row's outputs wait for all of its inputs),
-// 333 x 8208 with an fp32 residual 7.4 us, one row 2.1 us of the GPU and 4.2 a
+// 333 x 8208 with an fp32 residual 7.5 us, one row 2.2 us of the GPU and 4.5 a
 // call, which is the host's pace.  (A first version, one CTA a row and 8 columns
 // a thread, spent 37 instructions an element, mostly on reductions: 23.5 us at
 // 4608 x 3072.)

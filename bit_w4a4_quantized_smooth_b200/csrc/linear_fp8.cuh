@@ -14,10 +14,10 @@ namespace svdq {
 // 192 threads per CTA (320 with the FP8 output): warp 0 TMA producer, warp 1
 // TMEM owner and (even CTA) MMA issuer, the others epilogue; the roles, the
 // hand-offs and the abort drain are those of the 4-bit kernel (linear.cuh).
-// Tensor-bound: 348 GFLOP at 4608 x 3072 x 12288 take 122.0 us alone on B200
-// (2.85 PFLOP/s, 86 % of twice the measured bf16 rate; 129.5 with GELU and FP8
-// output) and 146 in a row, where the power limit holds the clock near 1.5 GHz;
-// 4608 x 12288 x 3072 115 and 138.
+// Tensor-bound: 348 GFLOP at 4608 x 3072 x 12288 take 123 us on B200 in a short
+// run of calls (2.82 PFLOP/s, 85 % of twice the measured bf16 rate; 131 with GELU
+// and FP8 output) and 152 with GELU in a long one, where the power limit holds
+// the clock near 1.5 GHz; 4608 x 12288 x 3072 119 and 137.
 // A tile is 24 stages of 11.4 thousand cycles together; the change to the next
 // (its last MMAs, one 64- or 128-column read of tensor memory, one arrival)
 // adds 1.9 thousand, the epilogue's arithmetic hides under the next tile.

@@ -12,8 +12,9 @@
 // splits, ... of every CTA's partial in rank order, adds the bias and stores
 // (bf16, or GELU and the FP8 block of the token's 128 channels, which is
 // exactly one warp's row).  No global scratch, and the sum's order is fixed.
-// On B200, weights from HBM: 1 x 3072 x 9216 takes 7.4 us (28.3 MB, 3.8 TB/s),
-// 1 x 3072 x 3072 4.4, 16 x 3072 x 12288 with GELU 9.1, 128 x 3072 x 3072 7.8.
+// On B200, weights from HBM: 1 x 3072 x 9216 takes 7.1 us in a stream of calls
+// (28.3 MB, 4.0 TB/s) and 7.5 in a graph; in a graph 1 x 3072 x 3072 4.7, 16 x
+// 3072 x 12288 with GELU 9.2, 128 x 3072 x 3072 7.9.
 // About 3 us of each are launch, first loads, exchange and stores, during which
 // the weights do not stream; a plain kernel that only loads 37.7 MB takes 8.5.
 #pragma once

@@ -313,9 +313,10 @@ svdq_status svdq_rmsnorm(const void* X, int64_t ldx, const void* residual, int r
 /*
  * 8-bit linear: Y = deq(x) deq(w)^T + bias as bf16.  The products are exact and
  * summed by the tensor cores in fp32, which cut off toward zero: a sum is off by
- * at most (ceil(K / 32) + 8) 2^-23 of its terms' absolute sum, and on average by
- * 1.6e-7 of the result's norm at K = 3072 and 8.2e-7 at K = 12288 (an fp32
- * product that rounds to nearest: 0.7e-7 and 1.6e-7).
+ * at most (ceil(K / 32) + 8) 2^-23 of its terms' absolute sum.  Measured against
+ * 64 bits, relative to the result's norm: 1.6e-7 at K = 3072 and 8.3e-7 at K =
+ * 12288 in the large-M kernel, 0.8e-7 and 1.7e-7 for one token in the few-rows
+ * kernel, whose CTAs sum a part of K each (svdq_set_linear_fp8_path forces it).
  *   x_codes, x_scales   FP8 block-128 of M rows of length K
  *   w_codes, w_scales   from svdq_pack_weight_fp8 (N rows)
  *   bias                bf16 [N] or NULL (added in fp32)
@@ -328,8 +329,9 @@ svdq_status svdq_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, con
 /*
  * 8-bit linear whose epilogue is the next layer's activation step:
  * GELU(deq(x) deq(w)^T + bias), taken in fp32 (GELU as svdq_quantize_fp8), to
- * FP8 block-128 along N.  The sum as in svdq_linear_fp8: its error moves about 5
- * codes in a million to a neighbour at K = 3072.
+ * FP8 block-128 along N.  The sum as in svdq_linear_fp8: in the large-M kernel
+ * its error moves 5 to 7 codes in a million to a neighbour at K = 3072 (fp32
+ * products and sums that round to nearest: 3).
  *   y_codes   uint8 [M][N] output;   y_scales   svdq_fp8_sizes(M, N) output
  * N a multiple of 16, N <= 2^20.
  */
@@ -363,8 +365,9 @@ svdq_status svdq_set_linear_fp8_splits(int splits);
 
 /*
  * Launch overlap of the layer calls (host-side setting for the whole
- * process; 1 by default).  With 1, svdq_quantize_act(_gelu, _noalloc) and
- * svdq_linear(_scaled) launch their kernels with CUDA's programmatic
+ * process; 1 by default).  With 1, svdq_quantize_act(_gelu, _noalloc),
+ * svdq_linear(_scaled) and the 8-bit layer's calls launch their kernels with
+ * CUDA's programmatic
  * stream-serialisation attribute: a kernel may be scheduled while the
  * kernel ahead of it in the stream is finishing, sets up (barriers, tensor
  * memory; the linear kernels also prefetch their weight tiles into L2) and
