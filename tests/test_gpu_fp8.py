@@ -1111,3 +1111,78 @@ def test_quantize_gelu_many_rows(M, K):
     _ok()
     g = ref.gelu(_np(X))
     ref.assert_encodes(_np(codes), _np(scales), g, np.abs(g) * GELU_REL)
+
+
+@pytest.mark.parametrize("M,K,N", [(1 << 22, 16, 16), (3, 16, 1 << 22), (3, 1 << 20, 16), (1, 16, 8)])
+def test_the_largest_and_the_smallest_sizes(M, K, N):
+    """Every size at its limit once, the others small; both kernels, both outputs."""
+    torch, svdq = _m()
+    gen = torch.Generator(device="cuda").manual_seed(M + N)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    X = rand(M, K).bfloat16()
+    W = rand(K, N) / K ** 0.5
+    rows = np.unique(np.concatenate([np.arange(min(M, 300)), np.arange(max(0, M - 300), M), np.arange(0, M, 65521)]))
+    cols = np.unique(np.concatenate([np.arange(min(N, 300)), np.arange(max(0, N - 300), N), np.arange(0, N, 65521)]))
+    rt, ct = torch.from_numpy(rows).cuda(), torch.from_numpy(cols).cuda()
+    (xc, xs), (wc, ws) = svdq.quantize_fp8(X), svdq.pack_weight_fp8(W)
+    _ok()
+    c, s = ref.encode(_np(X[rt]))
+    assert np.array_equal(_np(xc.view(torch.uint8)[rt]), c)
+    assert np.array_equal(ref.untile(_np(xs), M, K)[0][rows], s)
+    wr, wsr = ref.encode(np.ascontiguousarray(_np(W[:, ct]).T))
+    assert np.array_equal(_np(wc.view(torch.uint8)[ct]), wr)
+    assert np.array_equal(ref.untile(_np(ws), N, K)[0][cols], wsr)
+    xv, wv = ref.decode(c, s), ref.decode(wr, wsr)
+    y, acc = xv @ wv.T, (-(-K // 32) + 8) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv).T)
+    for path in ("large", "small"):
+        svdq.set_linear_fp8_path(path)
+        try:
+            Y = svdq.linear_fp8(xc, xs, wc, ws)
+            _ok()
+            _check_y(Y[rt][:, ct], y, acc)
+            del Y
+            if N % 16 == 0 and N <= 1 << 20:
+                codes, scales = svdq.linear_fp8_gelu(xc, xs, wc, ws)
+                _ok()
+                sc = ref.untile(_np(scales), M, N)[0][rows]
+                g = ref.gelu(y)
+                ref.assert_encodes(_np(codes.view(torch.uint8)[rt]), ref.tiles(sc), g, 1.13 * acc + np.abs(g) * GELU_REL)
+        finally:
+            svdq.set_linear_fp8_path("auto")
+    if K <= 32768:
+        Yn = svdq.rmsnorm(X, fp8_out=False, bf16_out=True, eps=1e-5)[3]
+        h = _np(X[rt])
+        n = h / np.sqrt((h * h).mean(axis=1, keepdims=True) + 1e-5)
+        got, err = _np(Yn[rt]), np.abs(n) * NORM_REL
+        assert (got >= ref.bf16_round(n - err)).all() and (got <= ref.bf16_round(n + err)).all()
+    _ok()
+
+
+def test_the_default_stream_and_foreign_streams_as_arguments():
+    """The stream argument may be the default stream while another is current, or
+    a stream that torch did not make."""
+    import ctypes
+    torch, svdq = _m()
+    rng = np.random.default_rng(31)
+    L = _mlp_weights(svdq, torch, rng, 512, 1040)
+    X, R = (_dev(rng.normal(size=(20, 512)), torch.bfloat16) for _ in range(2))
+    want = _mlp(svdq, L, X, R.clone())
+    torch.cuda.synchronize()
+    rt, h = ctypes.CDLL("libcudart.so.12"), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(h), 1) == 0
+    try:
+        for st in (torch.cuda.default_stream(), torch.cuda.ExternalStream(h.value)):
+            r = R.clone()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(torch.cuda.Stream()):
+                xc, xs, _, _ = svdq.rmsnorm(X, L["gamma"], r, residual_out=r, stream=st)
+                hc, hs = svdq.linear_fp8_gelu(xc, xs, L["uc"], L["us"], L["ub"], stream=st)
+                y = svdq.linear_fp8(hc, hs, L["dc"], L["ds"], L["db"], stream=st)
+            st.synchronize()
+            assert torch.equal(y, want)
+            del xc, xs, hc, hs, y
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()                               # the foreign stream's blocks
+    finally:
+        assert rt.cudaStreamDestroy(h) == 0
+    _ok()
