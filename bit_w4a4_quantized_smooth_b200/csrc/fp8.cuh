@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx_fp8.cuh"
 
 namespace svdq {
 
