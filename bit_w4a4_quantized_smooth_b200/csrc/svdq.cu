@@ -645,8 +645,9 @@ svdq_status launch_rmsnorm(const void* X, int64_t ldx, const void* residual, con
   // K = 4096 with a bf16 residual and FP8 output, one against two, by segments
   // an SM: 5.9 and 6.6 us at 40, 11.6 and 11.8 at 100, 14.1 and 14.0 at 130,
   // 16.5 and 16.2 at 160, 28.3 and 27.2 at 300, 86.8 and 79.6 at 1000 (K = 1024
-  // and 3072 within 3 % of that).  With an fp32 residual one stays better, 28.9
-  // and 30.0 at 200, 64.5 and 65.4 at 500.  A row of one warp: four a CTA.
+  // and 3072 within 5 % of that; K = 8192, 16 warps a row, gains from two at 64
+  // already, 9.3 and 8.2).  With an fp32 residual one stays better, 28.9 and 30.0
+  // at 200, 64.5 and 65.4 at 500.  A row of one warp: four a CTA.
   const int dev = current_device();
   if (dev < 0) return SVDQ_ERR_CUDA;
   const int sms = sm_count(dev);
